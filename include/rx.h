@@ -87,6 +87,39 @@ rx_status rx_store_kv(const rx_kv_desc* desc, void* k_pool, void* v_pool, const 
                       rx_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * The 8-bit pool: K and V rows as e4m3 codes with one float32 scale per (slot, KV head), 132 bytes
+ * a row where the bf16 pool takes 256 -- nearly twice the cached tokens in the same memory, and
+ * half the bytes for a decode to read.  (The pages keep the cache in the model's type; this is an
+ * addition of the library's own.)  It is a second pool type, not a view of the bf16 pool: same
+ * slots, same req_to_token table, calls of its own.  All (device), caller-owned, 16-byte aligned:
+ *   k_code, v_code    [pool_size, num_kv_heads, head_dim] e4m3
+ *   k_scale, v_scale  [pool_size, num_kv_heads] float32
+ * Value x of a row stands for code * scale.  What the calls below read holds no NaN codes (0x7f,
+ * 0xff); a NaN scale makes its whole row NaN. */
+typedef struct {
+  void* k_code;
+  void* v_code;
+  float* k_scale;
+  float* v_scale;
+} rx_kv_q8;
+
+/* rx_store_kv_q8 -- quantise the KV of new tokens into their slots of an 8-bit pool; arguments as
+ * rx_store_kv (k_new, v_new bf16).  Per row of 128 values, with a = max |x|:
+ *   scale = max(a / 448, 2^-126),   code = e4m3(x * r), round to nearest even, saturating,
+ * where r = 448 / a in float32 (2^126 at the scale's floor).  A row with an infinity or a NaN gets
+ * scale NaN and codes 0.  Out-of-pool and duplicate slots as rx_store_kv (a duplicate's row is one
+ * writer's codes, and one writer's scale: they need not be the same writer's). */
+rx_status rx_store_kv_q8(const rx_kv_desc* desc, const rx_kv_q8* kv, const void* k_new,
+                         const void* v_new, const int32_t* slots, int64_t num_tokens,
+                         rx_stream_t stream);
+/* rx_load_kv_q8 -- read slots of an 8-bit pool back: k_out[t] = bf16(code * scale) of slot
+ * slots[t], and v_out; k_out, v_out (device) [num_tokens, num_kv_heads, head_dim] bf16, 16-byte
+ * aligned.  A slot may be named any number of times; one outside the pool reads as zeros.
+ * num_tokens == 0 is a no-op. */
+rx_status rx_load_kv_q8(const rx_kv_desc* desc, const rx_kv_q8* kv, const int32_t* slots,
+                        int64_t num_tokens, void* k_out, void* v_out, rx_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Plans.  Attention work is split into work items on the host from host copies of the lengths
  * (the radix-tree match that produces them runs on the CPU as well: SGLang explainer, RadixAttention
  * -- the tree is kept on the CPU).  A plan is built once per batch, uploaded into the caller's
@@ -108,6 +141,14 @@ void rx_plan_destroy(rx_plan* plan);
 #define RX_EXTEND_TILES 0
 #define RX_EXTEND_PAIR 1
 rx_status rx_plan_set_extend_kernel(rx_plan* plan, int32_t kernel);
+/* Which pool the plans built on `plan` after this call are for (host; the plan's existing tables are
+ * not changed): RX_KV_BF16 (default; rx_extend_attn, rx_decode_attn) or RX_KV_E4M3, the 8-bit pool
+ * (rx_extend_attn_q8, rx_decode_attn_q8).  A call of the other type is refused with RX_ERR_INVALID,
+ * as is any other value here.  An extend plan for the 8-bit pool with RX_EXTEND_PAIR set is refused
+ * with RX_ERR_UNSUPPORTED when it is built. */
+#define RX_KV_BF16 0
+#define RX_KV_E4M3 1
+rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
  * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
@@ -217,6 +258,15 @@ rx_status rx_decode_plan(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
 rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void* k_pool,
                          const void* v_pool, const void* q, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, rx_stream_t stream);
+
+/* rx_decode_attn_q8 -- rx_decode_attn over an 8-bit pool, for a decode plan built for RX_KV_E4M3:
+ *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
+ *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
+ * with fp32 sums of exact products of the codes.  A key whose K scale is NaN makes o and lse of
+ * the requests that read it NaN, a NaN V scale their o. */
+rx_status rx_decode_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
+                            const void* q, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, rx_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * rx_decode_attn_noalloc -- rx_decode_attn for callers that cannot allocate device memory.

@@ -1,0 +1,212 @@
+// rx_store_kv_q8 / rx_load_kv_q8: the 8-bit pool's scatter and gather.
+//
+// A row is the 128 values of one (token, KV head) of K or of V.  With a = max |x| over the row:
+//   scale = max(a / 448, 2^-126),  code = e4m3(x * r),  r = 448 / a  (2^126 at the scale's floor),
+// so the largest value takes the largest code, 448, and every code is within half an e4m3 step of
+// x / scale.  448 is e4m3's largest value; the floor keeps scale and r normal numbers, for a row
+// of zeros too.  Reading back is code * scale, rounded once to bf16.  A row with an infinity or a
+// NaN has no such scale: its scale is NaN and its codes 0, so it reads as NaN.
+//
+// Both kernels move data: 256 + 132 bytes a row.  Eight (store) or sixteen (load) lanes share a
+// row, so that a lane's wider side is 16-byte accesses and a row's maximum takes three shuffles;
+// K and V are the two halves of the grid's y axis, and a thread has the loads of all its rows in
+// flight before the first is used.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+#include "rx_internal.h"
+
+namespace rx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+
+// Two fp32 values -> two e4m3 codes (round to nearest even, saturating), lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A position in the flat list of rows, moved on by a fixed stride without divisions.
+struct RowIter {
+  int64_t row, token;
+  int head;
+  __device__ RowIter(int64_t r, int hkv) : row(r), token(r / hkv), head((int)(r - token * hkv)) {}
+  __device__ void step(int64_t rows, int64_t tokens, int heads, int hkv) {
+    row += rows;
+    token += tokens;
+    head += heads;
+    if (head >= hkv) {
+      head -= hkv;
+      ++token;
+    }
+  }
+};
+
+template <int U>
+__global__ void __launch_bounds__(kThreads) store_q8_kernel(
+    uint8_t* __restrict__ k_code, uint8_t* __restrict__ v_code, float* __restrict__ k_scale,
+    float* __restrict__ v_scale, const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+    const int32_t* __restrict__ slots, int64_t n_rows, int hkv, int64_t pool_size) {
+  const bool is_v = blockIdx.y != 0;
+  const uint4* src = is_v ? v_new : k_new;
+  uint8_t* code = is_v ? v_code : k_code;
+  float* scale = is_v ? v_scale : k_scale;
+  const int l = threadIdx.x & 7;  // lane of the row: values 16 l .. 16 l + 15
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 8);
+  const int64_t st_tokens = stride / hkv;
+  const int st_heads = (int)(stride - st_tokens * hkv);
+  RowIter it((int64_t)blockIdx.x * (kThreads / 8) + threadIdx.x / 8, hkv);
+  // the eight lanes of a row leave together; a warp's four rows may not, hence the group's mask
+  const uint32_t group = 0xffu << (threadIdx.x & 24);
+  while (it.row < n_rows) {
+    uint4 x[U][2];
+    int64_t dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      dst[u] = -1;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+      if (it.row < n_rows) {
+        const int64_t s = __ldg(slots + it.token);
+        if (s >= 0 && s < pool_size) {
+          dst[u] = s * hkv + it.head;
+          x[u][0] = __ldcs(src + it.row * 16 + 2 * l);
+          x[u][1] = __ldcs(src + it.row * 16 + 2 * l + 1);
+        }
+      }
+      it.step(stride, st_tokens, st_heads, hkv);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w,
+                             x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+      // the order of bf16 magnitudes is that of their bits; an infinity or a NaN ends at 0x7f80
+      // or above
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(group, m, off));
+      const uint32_t top = max(m & 0xffffu, m >> 16);
+      const float a = __uint_as_float(top << 16);
+      const bool fine = top < 0x7f80u;
+      const float sc = fmaxf(a / kE4m3Max, kMinScale);
+      const float r = sc > kMinScale ? kE4m3Max / a : 1.f / kMinScale;
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = e4m3x2(bf_lo(w[2 * i]) * r, bf_hi(w[2 * i]) * r) |
+               e4m3x2(bf_lo(w[2 * i + 1]) * r, bf_hi(w[2 * i + 1]) * r) << 16;
+        if (!fine) c[i] = 0;
+      }
+      if (dst[u] >= 0) {
+        *reinterpret_cast<uint4*>(code + dst[u] * kHeadDim + 16 * l) =
+            make_uint4(c[0], c[1], c[2], c[3]);
+        if (l == 0) scale[dst[u]] = fine ? sc : __uint_as_float(0x7fc00000u);
+      }
+    }
+  }
+}
+
+template <int U>
+__global__ void __launch_bounds__(kThreads) load_q8_kernel(
+    const uint8_t* __restrict__ k_code, const uint8_t* __restrict__ v_code,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+    const int32_t* __restrict__ slots, uint4* __restrict__ k_out, uint4* __restrict__ v_out,
+    int64_t n_rows, int hkv, int64_t pool_size) {
+  const bool is_v = blockIdx.y != 0;
+  const uint8_t* code = is_v ? v_code : k_code;
+  const float* scale = is_v ? v_scale : k_scale;
+  uint4* out = is_v ? v_out : k_out;
+  const int l = threadIdx.x & 15;  // lane of the row: values 8 l .. 8 l + 7
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 16);
+  const int64_t st_tokens = stride / hkv;
+  const int st_heads = (int)(stride - st_tokens * hkv);
+  RowIter it((int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16, hkv);
+  while (it.row < n_rows) {
+    uint2 c[U];
+    float sc[U];
+    const int64_t first = it.row;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      c[u] = make_uint2(0, 0);
+      sc[u] = 0.f;
+      if (it.row < n_rows) {
+        const int64_t s = __ldg(slots + it.token);
+        if (s >= 0 && s < pool_size) {  // a slot outside the pool reads as zeros
+          const int64_t r = s * hkv + it.head;
+          c[u] = __ldg(reinterpret_cast<const uint2*>(code + r * kHeadDim) + l);
+          sc[u] = __ldg(scale + r);
+        }
+      }
+      it.step(stride, st_tokens, st_heads, hkv);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = first + u * stride;
+      if (row >= n_rows) break;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = ((i < 2 ? c[u].x : c[u].y) >> (16 * (i & 1))) & 0xffffu;
+        const float2 f = e4m3x2_to_f32(pair);
+        w[i] = pack_bf16(f.x * sc[u], f.y * sc[u]);
+      }
+      __stcs(out + row * 16 + l, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+}  // namespace
+
+int launch_store_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const void* k_new,
+                       const void* v_new, const int32_t* slots, int64_t n, void* stream) {
+  if (n == 0) return 0;
+  const int64_t rows = n * d->num_kv_heads;
+  const int sms = sm_count();
+  if (sms == 0) return (int)cudaGetLastError();
+  constexpr int kRows = kThreads / 8;
+  auto run = [&](auto kernel, int u) {
+    const int64_t blocks = (rows + (int64_t)kRows * u - 1) / ((int64_t)kRows * u);
+    const dim3 grid((unsigned)(blocks < 4LL * sms ? blocks : 4LL * sms), 2);
+    kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
+        (uint8_t*)kv->k_code, (uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, (const uint4*)k_new,
+        (const uint4*)v_new, slots, rows, d->num_kv_heads, d->pool_size);
+    return (int)cudaGetLastError();
+  };
+  return run(store_q8_kernel<4>, 4);
+}
+
+int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* slots, int64_t n,
+                      void* k_out, void* v_out, void* stream) {
+  if (n == 0) return 0;
+  const int64_t rows = n * d->num_kv_heads;
+  const int sms = sm_count();
+  if (sms == 0) return (int)cudaGetLastError();
+  constexpr int kRows = kThreads / 16;
+  auto run = [&](auto kernel, int u) {
+    const int64_t blocks = (rows + (int64_t)kRows * u - 1) / ((int64_t)kRows * u);
+    const dim3 grid((unsigned)(blocks < 4LL * sms ? blocks : 4LL * sms), 2);
+    kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
+        (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, slots,
+        (uint4*)k_out, (uint4*)v_out, rows, d->num_kv_heads, d->pool_size);
+    return (int)cudaGetLastError();
+  };
+  return run(load_q8_kernel<4>, 4);
+}
+
+}  // namespace rx

@@ -91,6 +91,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct rx_plan {
   int kind = 0;  // 0 = empty, 1 = extend, 2 = decode
   int32_t ext_kernel = RX_EXTEND_TILES;  // the kernel extend plans built from now on run on
+  int32_t kv_next = RX_KV_BF16;          // the pool type plans built from now on are for
+  int32_t kv_type = RX_KV_BF16;          // the pool type the built plan is for
   std::vector<uint8_t> blob;  // header + tables, uploaded verbatim
   size_t ws_bytes = 0;
   int64_t key_reads = 0;  // (key, KV head) rows of the pool the kernels read
@@ -165,6 +167,7 @@ void put(std::vector<uint8_t>& blob, int64_t off, const std::vector<T>& v) {
 }
 
 void remember_desc(rx_plan* p, const rx_kv_desc* d) {
+  p->kv_type = p->kv_next;
   p->hq = d->num_q_heads;
   p->hkv = d->num_kv_heads;
   p->rows = d->req_to_token_rows;
@@ -173,12 +176,27 @@ void remember_desc(rx_plan* p, const rx_kv_desc* d) {
   p->table = d->req_to_token;
 }
 
-rx_status check_plan_use(const rx_plan* p, int kind, const rx_kv_desc* d, const void* k,
+// The pointers of an 8-bit pool.
+rx_status check_kv_q8(const rx_kv_q8* kv) {
+  if (!kv) return fail(RX_ERR_INVALID, "kv is NULL");
+  if (!kv->k_code || !kv->v_code || !kv->k_scale || !kv->v_scale)
+    return fail(RX_ERR_INVALID, "NULL code or scale pointer");
+  if (!aligned16(kv->k_code) || !aligned16(kv->v_code) || !aligned16(kv->k_scale) ||
+      !aligned16(kv->v_scale))
+    return fail(RX_ERR_INVALID, "codes and scales must be 16-byte aligned");
+  return RX_OK;
+}
+
+rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_kv_desc* d,
+                         const void* k,
                          const void* v, const void* q, const void* o, const void* lse,
                          const void* ws, size_t ws_bytes) {
   if (!p) return fail(RX_ERR_INVALID, "plan is NULL");
   if (p->kind != kind)
     return fail(RX_ERR_INVALID, "plan was built for %s", p->kind == 1 ? "extend" : p->kind == 2 ? "decode" : "nothing");
+  if (p->kv_type != kv_type)
+    return fail(RX_ERR_INVALID, "plan was built for a %s pool (rx_plan_set_kv_type)",
+                p->kv_type == RX_KV_E4M3 ? "8-bit" : "bf16");
   rx_status st = check_desc(d, true);
   if (st) return st;
   if (d->num_q_heads != p->hq || d->num_kv_heads != p->hkv || d->req_to_token_rows != p->rows ||
@@ -234,7 +252,8 @@ rx_status rx::plan_for_noalloc(const rx_plan* plan, const rx_kv_desc* desc, cons
                 "rx_decode_attn_noalloc: the plan needs %zu bytes of scratch, the library holds "
                 "%zu; use rx_decode_attn with a workspace for batches this large",
                 plan->ws_bytes, scratch_bytes);
-  rx_status st = check_plan_use(plan, 2, desc, k, v, q, o, lse, scratch, scratch_bytes);
+  rx_status st = check_plan_use(plan, 2, RX_KV_BF16, desc, k, v, q, o, lse, scratch,
+                                scratch_bytes);
   if (st) return st;
   *hdr = plan->hdr();
   return RX_OK;
@@ -273,6 +292,39 @@ rx_status rx_store_kv(const rx_kv_desc* desc, void* k_pool, void* v_pool, const 
   return e ? cuda_fail(e, "store_kv launch") : RX_OK;
 }
 
+rx_status rx_store_kv_q8(const rx_kv_desc* desc, const rx_kv_q8* kv, const void* k_new,
+                         const void* v_new, const int32_t* slots, int64_t num_tokens,
+                         rx_stream_t stream) {
+  rx_status st = check_desc(desc, false);
+  if (st) return st;
+  if (num_tokens < 0) return fail(RX_ERR_INVALID, "num_tokens < 0");
+  if (num_tokens == 0) return RX_OK;
+  st = check_kv_q8(kv);
+  if (st) return st;
+  if (!k_new || !v_new || !slots) return fail(RX_ERR_INVALID, "NULL pointer");
+  if (!aligned16(k_new) || !aligned16(v_new))
+    return fail(RX_ERR_INVALID, "K/V pointers must be 16-byte aligned");
+  if (num_tokens > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "num_tokens >= 2^31");
+  const int e = launch_store_kv_q8(desc, kv, k_new, v_new, slots, num_tokens, stream);
+  return e ? cuda_fail(e, "store_kv_q8 launch") : RX_OK;
+}
+
+rx_status rx_load_kv_q8(const rx_kv_desc* desc, const rx_kv_q8* kv, const int32_t* slots,
+                        int64_t num_tokens, void* k_out, void* v_out, rx_stream_t stream) {
+  rx_status st = check_desc(desc, false);
+  if (st) return st;
+  if (num_tokens < 0) return fail(RX_ERR_INVALID, "num_tokens < 0");
+  if (num_tokens == 0) return RX_OK;
+  st = check_kv_q8(kv);
+  if (st) return st;
+  if (!k_out || !v_out || !slots) return fail(RX_ERR_INVALID, "NULL pointer");
+  if (!aligned16(k_out) || !aligned16(v_out))
+    return fail(RX_ERR_INVALID, "K/V pointers must be 16-byte aligned");
+  if (num_tokens > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "num_tokens >= 2^31");
+  const int e = launch_load_kv_q8(desc, kv, slots, num_tokens, k_out, v_out, stream);
+  return e ? cuda_fail(e, "load_kv_q8 launch") : RX_OK;
+}
+
 rx_status rx_plan_create(rx_plan** out) {
   if (!out) return fail(RX_ERR_INVALID, "out is NULL");
   *out = new rx_plan();
@@ -286,6 +338,14 @@ rx_status rx_plan_set_extend_kernel(rx_plan* plan, int32_t kernel) {
   if (kernel != RX_EXTEND_TILES && kernel != RX_EXTEND_PAIR)
     return fail(RX_ERR_INVALID, "unknown extend kernel");
   plan->ext_kernel = kernel;
+  return RX_OK;
+}
+
+rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type) {
+  if (!plan) return fail(RX_ERR_INVALID, "plan is NULL");
+  if (kv_type != RX_KV_BF16 && kv_type != RX_KV_E4M3)
+    return fail(RX_ERR_INVALID, "unknown pool type");
+  plan->kv_next = kv_type;
   return RX_OK;
 }
 
@@ -444,12 +504,15 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   std::vector<int32_t> rows;
   std::vector<std::vector<DecMergeRef>> refs(batch);
   int64_t npart = 0;
-  const int max_tok = 64 / gq;
-  auto kind_of_rows = [](int r) { return r <= 16 ? 0 : (r <= 32 ? 1 : 2); };
-  auto hb_of = [](int kind) { return kind == 0 ? 8 : (kind == 1 ? 4 : 2); };
+  // 8-bit pools have kinds, head blocks and splits of their own (see kQ8WarpKeys)
+  const bool q8 = plan->kv_next == RX_KV_E4M3;
+  const int q8_hb = 1 << q8_head_block_log2(hkv), splits = q8 ? 8 / q8_hb : 1;
+  const int max_tok = (q8 ? kQ8MaxRows : 64) / gq;
+  auto kind_of_rows = [&](int r) { return q8 ? r > 8 : r <= 16 ? 0 : (r <= 32 ? 1 : 2); };
+  auto hb_of = [&](int kind) { return q8 ? q8_hb : kind == 0 ? 8 : (kind == 1 ? 4 : 2); };
 
   // bytes of K+V per key for one KV head
-  const double key_bytes = 2.0 * kHeadDim * 2;
+  const double key_bytes = q8 ? 2.0 * (kHeadDim + 4) : 2.0 * kHeadDim * 2;
   double total = 0;
   for (int g = 0; g < num_groups; ++g)
     if (!members[g].empty() && group_prefix_len[g] > node_lo(g))
@@ -463,17 +526,23 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
 
   auto chunks = [&](int len, int kind, std::vector<std::pair<int, int>>& out) {
     const int hb = std::min(hb_of(kind), hkv);
-    const int nk = kDecRows / hb_of(kind);
+    const int nk = q8 ? splits * kQ8WarpKeys : kDecRows / hb_of(kind);
     int max_keys = (int)(target / (hb * key_bytes));
-    max_keys = std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
+    max_keys = q8 ? std::max(2 * nk, max_keys)
+                  : std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
     const int n = (len + max_keys - 1) / max_keys;
     int c = (len + n - 1) / n;
     c = (c + nk - 1) / nk * nk;
-    c = std::min(c, kDecMaxKeysPerItem);
+    if (!q8) c = std::min(c, kDecMaxKeysPerItem);
     out.clear();
     for (int k = 0; k < len; k += c) out.push_back({k, std::min(len, k + c)});
   };
   std::vector<std::pair<int, int>> ch;
+  // The references of one request to a unit of `len` keys: one partial per split that has keys.
+  auto refer = [&](int b, int64_t part, int len, int n_rows, int row) {
+    for (int k = 0; k < splits && k * kQ8WarpKeys < len; ++k)
+      refs[b].push_back({(int32_t)(part + (int64_t)k * hkv * n_rows), n_rows, row, 0});
+  };
 
   // Shared-prefix units whose stacked query rows reach 32 per KV head run on the tensor-core
   // attention kernel (128 / gq requests per tile, two tiles per item, one KV head per item, about
@@ -488,7 +557,7 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     const int lo = node_lo(g), hi = group_prefix_len[g];
     const auto& mem = members[g];
     if (mem.empty() || hi <= lo) continue;
-    if (tc_ok && (int64_t)mem.size() * gq >= 32) {
+    if (tc_ok && !q8 && (int64_t)mem.size() * gq >= 32) {
       struct XTile {
         int row_begin, n_tok, t0;
       };
@@ -542,11 +611,11 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
       chunks(hi - lo, kind, ch);
       for (auto& c : ch) {
         const int64_t part = npart;
-        npart += (int64_t)hkv * n_tok * gq;
+        npart += (int64_t)splits * hkv * n_tok * gq;
         units.push_back(
             {kind, req_idx[mem[t0]], lo + c.first, lo + c.second, row_begin, n_tok, part});
         for (int i = 0; i < n_tok; ++i)
-          refs[mem[t0 + i]].push_back({(int32_t)part, n_tok * gq, i * gq, 0});
+          refer(mem[t0 + i], part, c.second - c.first, n_tok * gq, i * gq);
       }
     }
   }
@@ -558,9 +627,9 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     chunks(seq_len[b] - k0, 0, ch);
     for (auto& c : ch) {
       const int64_t part = npart;
-      npart += (int64_t)hkv * gq;
+      npart += (int64_t)splits * hkv * gq;
       units.push_back({0, req_idx[b], k0 + c.first, k0 + c.second, row_begin, 1, part});
-      refs[b].push_back({(int32_t)part, gq, 0, 0});
+      refer(b, part, c.second - c.first, gq, 0);
     }
   }
   if (npart > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
@@ -595,6 +664,7 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   std::memset(&h, 0, sizeof h);
   h.magic = kPlanMagic;
   h.kind = 2;
+  h.kv_type = plan->kv_next;
   h.n_items = (int32_t)items.size();
   h.num_q_heads = desc->num_q_heads;
   h.num_kv_heads = hkv;
@@ -634,7 +704,7 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
 rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void* k_pool,
                          const void* v_pool, const void* q, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, rx_stream_t stream) {
-  rx_status st = check_plan_use(plan, 2, desc, k_pool, v_pool, q, o, lse, workspace,
+  rx_status st = check_plan_use(plan, 2, RX_KV_BF16, desc, k_pool, v_pool, q, o, lse, workspace,
                                 workspace_bytes);
   if (st) return st;
   const PlanHeader h = plan->hdr();
@@ -642,6 +712,19 @@ rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
   st = plan_aux_stream(plan, &aux);
   if (st) return st;
   const int e = launch_decode(desc, &h, k_pool, v_pool, q, o, lse, workspace, stream, &aux);
+  return e ? cuda_fail(e, "decode launch") : RX_OK;
+}
+
+rx_status rx_decode_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
+                            const void* q, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, rx_stream_t stream) {
+  rx_status st = check_kv_q8(kv);
+  if (st) return st;
+  st = check_plan_use(plan, 2, RX_KV_E4M3, desc, kv->k_code, kv->v_code, q, o, lse, workspace,
+                      workspace_bytes);
+  if (st) return st;
+  const PlanHeader h = plan->hdr();
+  const int e = launch_decode_q8(desc, &h, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "decode launch") : RX_OK;
 }
 
@@ -916,6 +999,7 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   std::memset(&h, 0, sizeof h);
   h.magic = kPlanMagic;
   h.kind = 1;
+  h.kv_type = plan->kv_next;
   h.ext_kernel = plan->ext_kernel;
   h.n_items = (int32_t)items.size();
   h.num_q_heads = desc->num_q_heads;
@@ -946,7 +1030,7 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
 rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void* k_pool,
                          const void* v_pool, const void* q, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, rx_stream_t stream) {
-  rx_status st = check_plan_use(plan, 1, desc, k_pool, v_pool, q, o, lse, workspace,
+  rx_status st = check_plan_use(plan, 1, RX_KV_BF16, desc, k_pool, v_pool, q, o, lse, workspace,
                                 workspace_bytes);
   if (st) return st;
   if (desc->pool_size * desc->num_kv_heads >= (int64_t)INT32_MAX)

@@ -47,6 +47,17 @@ constexpr int kDecRows = 128;                              // (head, key) rows p
 constexpr int kDecStageBytes = 2 * kDecRows * kHeadDim * 2;   // K + V, 128 rows each
 constexpr size_t kDecSmemBytes = (size_t)kDecStages * kDecStageBytes + kDecMaxKeysPerItem * 4;
 
+// Decode over an 8-bit pool: items of the same form, cut for decode_q8_kernel.  Its kinds are
+// tiles of 8 query rows: kind 0 one (up to 8 rows), kind 1 two.  Eight consumer warps take a KV
+// head each, 32 keys a stage; a block holds the largest power of two of heads (at most 8) that
+// divides num_kv_heads, and with fewer than 8 heads the warps split a stage's keys (8 / heads ways).
+// A work unit's partial rows: [split][KV head][row].
+constexpr int kQ8WarpKeys = 32;
+constexpr int kQ8MaxRows = 16;
+inline int q8_head_block_log2(int hkv) {
+  return hkv % 8 == 0 ? 3 : hkv % 4 == 0 ? 2 : hkv % 2 == 0 ? 1 : 0;
+}
+
 // ---------------------------------------------------------------------------------------------
 // Extend.  A row tile holds up to 128 query rows (new tokens x gq query heads of one KV head); a
 // work item pairs two row tiles with one list of key segments.  Segment owner -1 is visible to
@@ -108,7 +119,8 @@ struct PlanHeader {
   // extend plans on the one-SM kernel: per-CTA item lists, int32 [n_ctas + 1] starts into the
   // item table (which is stored CTA by CTA); n_ctas = 0 when the items are dealt in snake order
   int64_t off_cta;
-  int32_t n_ctas, pad32;
+  int32_t n_ctas;
+  int32_t kv_type;       // RX_KV_BF16 or RX_KV_E4M3: the pool the plan's calls read
   int64_t pad[13];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
@@ -125,6 +137,12 @@ struct AuxStream {
 // Launchers (defined in the .cu files).  Return cudaError_t as int.
 int launch_store_kv(const rx_kv_desc* d, void* k_pool, void* v_pool, const void* k_new,
                     const void* v_new, const int32_t* slots, int64_t n, void* stream);
+int launch_store_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const void* k_new,
+                       const void* v_new, const int32_t* slots, int64_t n, void* stream);
+int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* slots, int64_t n,
+                      void* k_out, void* v_out, void* stream);
+int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
+                     void* o, float* lse, void* ws, void* stream);
 int launch_decode(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                   const void* v_pool, const void* q, void* o, float* lse, void* ws,
                   void* stream, const AuxStream* aux);

@@ -19,15 +19,17 @@ LIB_PATH = os.path.join(_HERE, "_lib", "librx.so")
 RX_OK, RX_ERR_INVALID, RX_ERR_RANGE, RX_ERR_UNSUPPORTED, RX_ERR_CUDA, RX_ERR_TIMEOUT, \
     RX_ERR_WORKSPACE = range(7)
 RX_EXTEND_TILES, RX_EXTEND_PAIR = 0, 1
+RX_KV_BF16, RX_KV_E4M3 = 0, 1
 
 EXPORTED = [
-    "rx_status_string", "rx_last_error", "rx_store_kv", "rx_plan_create", "rx_plan_destroy",
-    "rx_plan_set_extend_kernel",
+    "rx_status_string", "rx_last_error", "rx_store_kv", "rx_store_kv_q8", "rx_load_kv_q8",
+    "rx_plan_create", "rx_plan_destroy",
+    "rx_plan_set_extend_kernel", "rx_plan_set_kv_type",
     "rx_plan_workspace_size", "rx_plan_upload", "rx_plan_key_reads", "rx_plan_launches",
     "rx_plan_rows",
     "rx_extend_plan",
     "rx_extend_plan_tree", "rx_extend_attn", "rx_decode_plan", "rx_decode_plan_tree",
-    "rx_decode_attn", "rx_decode_attn_noalloc", "rx_noalloc_read_status",
+    "rx_decode_attn", "rx_decode_attn_q8", "rx_decode_attn_noalloc", "rx_noalloc_read_status",
     "rx_noalloc_scratch_bytes", "rx_read_status", "rx_selftest_wait_timeout",
     "rx_selftest_pair_mma",
     "rx_check_slots", "rx_check_tables", "rx_radix_create", "rx_radix_destroy",
@@ -52,6 +54,11 @@ class KVDesc(C.Structure):
                 ("req_to_token_rows", C.c_int64), ("req_to_token_stride", C.c_int64)]
 
 
+class KVQ8(C.Structure):
+    _fields_ = [("k_code", C.c_void_p), ("v_code", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p)]
+
+
 _lib = None
 _P = C.c_void_p
 _I32P = C.POINTER(C.c_int32)
@@ -70,9 +77,14 @@ def lib():
         "rx_status_string": (C.c_char_p, [C.c_int]),
         "rx_last_error": (C.c_char_p, []),
         "rx_store_kv": (C.c_int, [C.POINTER(KVDesc), _P, _P, _P, _P, _P, C.c_int64, _P]),
+        "rx_store_kv_q8": (C.c_int, [C.POINTER(KVDesc), C.POINTER(KVQ8), _P, _P, _P, C.c_int64,
+                                     _P]),
+        "rx_load_kv_q8": (C.c_int, [C.POINTER(KVDesc), C.POINTER(KVQ8), _P, C.c_int64, _P, _P,
+                                    _P]),
         "rx_plan_create": (C.c_int, [C.POINTER(_P)]),
         "rx_plan_destroy": (None, [_P]),
         "rx_plan_set_extend_kernel": (C.c_int, [_P, C.c_int32]),
+        "rx_plan_set_kv_type": (C.c_int, [_P, C.c_int32]),
         "rx_plan_workspace_size": (C.c_int, [_P, C.POINTER(C.c_size_t)]),
         "rx_plan_upload": (C.c_int, [_P, _P, C.c_size_t, _P]),
         "rx_plan_key_reads": (C.c_int, [_P, _I64P]),
@@ -90,6 +102,8 @@ def lib():
                                      C.c_int32, _I32P]),
         "rx_decode_attn": (C.c_int, [_P, C.POINTER(KVDesc), _P, _P, _P, _P, _P, _P, C.c_size_t,
                                      _P]),
+        "rx_decode_attn_q8": (C.c_int, [_P, C.POINTER(KVDesc), C.POINTER(KVQ8), _P, _P, _P, _P,
+                                        C.c_size_t, _P]),
         "rx_decode_attn_noalloc": (C.c_int, [_P, C.POINTER(KVDesc), _P, _P, _P, _P, _P, _P]),
         "rx_noalloc_read_status": (C.c_int, [_I32P, _P]),
         "rx_noalloc_scratch_bytes": (C.c_size_t, []),
@@ -189,6 +203,69 @@ def store_kv(desc: KVDesc, k_pool, v_pool, k_new, v_new, slots, stream=None):
                              _ptr(slots), n, _stream(stream)))
 
 
+def kv_q8(k_code, v_code, k_scale, v_scale) -> KVQ8:
+    """An 8-bit pool (rx_kv_q8) from its CUDA tensors: codes [pool_size, Hkv, 128], one byte an
+    element (float8_e4m3fn or uint8), and float32 scales [pool_size, Hkv].  Keeps the tensors."""
+    shape = tuple(k_code.shape)
+    for name, t, want, size in (("k_code", k_code, shape, 1), ("v_code", v_code, shape, 1),
+                                ("k_scale", k_scale, shape[:2], 4),
+                                ("v_scale", v_scale, shape[:2], 4)):
+        if len(shape) != 3 or tuple(t.shape) != want or not t.is_contiguous():
+            raise ValueError(f"{name} of shape {tuple(t.shape)}: contiguous codes [pool_size, Hkv, "
+                             "128] and scales [pool_size, Hkv] expected")
+        if t.element_size() != size or str(t.dtype) not in (
+                ("torch.float8_e4m3fn", "torch.uint8") if size == 1 else ("torch.float32",)):
+            raise ValueError(f"{name} is {t.dtype}: float8_e4m3fn (or uint8) codes and float32 "
+                             "scales expected")
+    kv = KVQ8(_ptr(k_code), _ptr(v_code), _ptr(k_scale), _ptr(v_scale))
+    kv.tensors, kv.shape = (k_code, v_code, k_scale, v_scale), shape
+    return kv
+
+
+def _check_q8(desc: KVDesc, kv: KVQ8, named):
+    """An 8-bit call's tensors against the descriptor: the pool's shape, and per (name, tensor,
+    elements, dtype) size, dtype, layout and device.  Raw addresses (ints) and hand-made KVQ8
+    structures are the caller's responsibility."""
+    import torch
+    shape = getattr(kv, "shape", None)
+    if shape is not None and shape != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
+        raise ValueError(f"the pool is {shape}, the descriptor's "
+                         f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t, n, dtype in named + [("pool", t, t.numel(), t.dtype)
+                                      for t in getattr(kv, "tensors", ())]:
+        if not isinstance(t, torch.Tensor):
+            continue
+        if t.numel() != n:
+            raise ValueError(f"{name} holds {t.numel()} elements; {n} expected")
+        if t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dtype} expected, got {t.dtype}")
+        if not t.is_cuda or t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def store_kv_q8(desc: KVDesc, kv: KVQ8, k_new, v_new, slots, stream=None):
+    """rx_store_kv_q8: quantise bf16 rows k_new, v_new [n, Hkv, 128] into slots [n] of the pool."""
+    import torch
+    n = int(slots.shape[0]) if slots is not None else 0
+    row = n * desc.num_kv_heads * desc.head_dim
+    _check_q8(desc, kv, [("k_new", k_new, row, torch.bfloat16),
+                         ("v_new", v_new, row, torch.bfloat16), ("slots", slots, n, torch.int32)])
+    _check(lib().rx_store_kv_q8(C.byref(desc), C.byref(kv), _ptr(k_new), _ptr(v_new), _ptr(slots),
+                                n, _stream(stream)))
+
+
+def load_kv_q8(desc: KVDesc, kv: KVQ8, slots, k_out, v_out, stream=None):
+    """rx_load_kv_q8: read slots [n] of the pool back into bf16 rows k_out, v_out [n, Hkv, 128]."""
+    import torch
+    n = int(slots.shape[0]) if slots is not None else 0
+    row = n * desc.num_kv_heads * desc.head_dim
+    _check_q8(desc, kv, [("k_out", k_out, row, torch.bfloat16),
+                         ("v_out", v_out, row, torch.bfloat16), ("slots", slots, n, torch.int32)])
+    _check(lib().rx_load_kv_q8(C.byref(desc), C.byref(kv), _ptr(slots), n, _ptr(k_out),
+                               _ptr(v_out), _stream(stream)))
+
+
 class Plan:
     """rx_plan: host-built work list for one batch (extend or decode)."""
 
@@ -216,6 +293,11 @@ class Plan:
         """rx_plan_set_extend_kernel: RX_EXTEND_TILES (default) or RX_EXTEND_PAIR for the extend
         plans built from now on."""
         _check(lib().rx_plan_set_extend_kernel(self._h, int(kernel)))
+
+    def set_kv_type(self, kv_type: int):
+        """rx_plan_set_kv_type: RX_KV_BF16 (default) or RX_KV_E4M3, the pool that the plans built
+        from now on are for."""
+        _check(lib().rx_plan_set_kv_type(self._h, int(kv_type)))
 
     def workspace_size(self) -> int:
         n = C.c_size_t(0)
@@ -318,6 +400,21 @@ def decode_attn(plan: Plan, desc: KVDesc, k_pool, v_pool, q, o, lse, workspace, 
     _check(lib().rx_decode_attn(plan.handle, C.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q),
                                 _ptr(o), _ptr(lse), _ptr(workspace), _nbytes(workspace),
                                 _stream(stream)))
+
+
+def _attn_q8(call, plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream):
+    import torch
+    n = plan.rows() * desc.num_q_heads
+    _check_q8(desc, kv, [("q", q, n * desc.head_dim, torch.bfloat16),
+                         ("o", o, n * desc.head_dim, torch.bfloat16),
+                         ("lse", lse, n, torch.float32)])
+    _check(call(plan.handle, C.byref(desc), C.byref(kv), _ptr(q), _ptr(o), _ptr(lse),
+                _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def decode_attn_q8(plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream=None):
+    """rx_decode_attn_q8: decode over an 8-bit pool with a plan built for RX_KV_E4M3."""
+    _attn_q8(lib().rx_decode_attn_q8, plan, desc, kv, q, o, lse, workspace, stream)
 
 
 def decode_attn_noalloc(plan: Plan, desc: KVDesc, k_pool, v_pool, q, o, lse, stream=None):

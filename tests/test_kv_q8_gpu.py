@@ -1,0 +1,438 @@
+"""The 8-bit pool on the GPU against float64: store and read-back bit for bit, attention within
+bounds derived from its roundings.
+
+Bounds.  With u = 2^-8 (half a bf16 step) an output element may be off by u |o| for its own
+rounding.  The weights of the decode's second product are fp16: off by 2^-11 of their value, or,
+below 2^-14 of the largest term, by 2^-25 of it.  A score is a float32 sum of exact products over
+128 values; 16 roundings of partial sums of at most S = scale * sum |q_d k_d|, each 2^-23 (the
+tensor core's accumulator truncates), move it by 2^-19 S, and the exponentials and logarithms by
+2^-19; a weight is the ratio of two such terms.  The extend's weights are bf16: 2^-9 of their value
+(round to nearest of 8 significant bits), times the V scale's own rounding, 2^-24.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as A, quantised as Q
+from prefix_shared_kv_gb300 import rx, workloads as W
+from prefix_shared_kv_gb300.session import bits_of, to_bf16, to_i32, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+class Pool:
+    """A random 8-bit pool on the host and on the device, and a descriptor over `table`."""
+
+    def __init__(self, cuda, rng, hq, hkv, pool_size, table):
+        self.hq, self.hkv, self.n = hq, hkv, pool_size
+        self.table, self.scale = np.ascontiguousarray(table, np.int32), 128 ** -0.5
+        k = rng.standard_normal((pool_size, hkv, 128)).astype(np.float32)
+        v = rng.standard_normal((pool_size, hkv, 128)).astype(np.float32)
+        k[:, :, ::37] *= 3
+        v *= np.exp(rng.standard_normal((pool_size, hkv, 1))).astype(np.float32)
+        self.kc, self.ks = Q.quantise(W.bf16_bits(k))
+        self.vc, self.vs = Q.quantise(W.bf16_bits(v))
+        self.cuda = cuda
+        self.upload()
+
+    def upload(self):
+        dev = self.cuda
+        self.dev = [torch.from_numpy(a).to(dev) for a in (self.kc, self.vc, self.ks, self.vs)]
+        self.kv = rx.kv_q8(*self.dev)
+        self.r2t = to_i32(self.table, dev)
+        self.desc = rx.kv_desc(self.hq, self.hkv, self.n, self.r2t, self.scale)
+
+    def rows(self, at):
+        """K, V and V scales of slots `at`; slots outside the pool are zeros."""
+        ok = (at >= 0) & (at < self.n)
+        at = np.where(ok, at, 0)
+        z = ok[:, None, None]
+        return (np.where(z, Q.values(self.kc[at], self.ks[at]), 0.0),
+                np.where(z, Q.values(self.vc[at], self.vs[at]), 0.0),
+                np.where(ok[:, None], self.vs[at].astype(np.float64), 0.0))
+
+    def check(self, o, lse, q, req_row, keys, visible, weight_err, what=""):
+        """o, lse [n, hq(, 128)] of one request's query rows against the definition."""
+        K, V, vs = self.rows(self.table[req_row, :keys].astype(np.int64))
+        got, got_l = A.bf16_to_f64(bits_of(o)), lse.double().cpu().numpy()
+        qf = A.bf16_to_f64(q)
+        gq = self.hq // self.hkv
+        for h in range(self.hq):
+            kh = h // gq
+            ro, rl, pv, sabs, big = Q.attend_rows(qf[:, h], K[:, kh], V[:, kh], vs[:, kh], visible,
+                                                  self.scale)
+            e_s = 2.0 ** -19 * sabs + 2.0 ** -19
+            tol = (2.0 ** -8 * np.abs(ro) + (weight_err + 2 * e_s)[:, None] * pv * 1.01
+                   + (keys * 2.0 ** -25 * 448 * big)[:, None])
+            err = np.abs(got[:, h] - ro)
+            assert (err <= tol + 1e-30).all(), (what, h, float((err / (tol + 1e-30)).max()))
+            lerr = np.abs(got_l[:, h] - rl)
+            fin = np.isfinite(rl)
+            assert (got_l[~fin, h] == rl[~fin]).all()
+            ltol = e_s + 2.0 ** -22 * np.abs(np.where(fin, rl, 0))
+            assert (lerr[fin] <= ltol[fin]).all(), (what, h, float(lerr[fin].max()))
+
+
+def random_table(rng, pool_size, lens, shared=None):
+    """Rows of distinct random slots; requests of `shared` = {group: (members, prefix)} share."""
+    perm = rng.permutation(pool_size).astype(np.int32)
+    at, table = 0, np.zeros((len(lens), max(1, max(lens, default=1)) + 3), np.int32)
+    for members, prefix in (shared or {}).values():
+        for b in members:
+            table[b, :prefix] = perm[at:at + prefix]
+        at += prefix
+    start = np.zeros(len(lens), int)
+    for members, prefix in (shared or {}).values():
+        start[members] = prefix
+    for b, n in enumerate(lens):
+        own = n - start[b]
+        table[b, start[b]:n] = perm[at:at + own]
+        at += own
+    assert at <= pool_size
+    return table
+
+
+# ---- store and load ---------------------------------------------------------------------------
+
+def _special_rows(bits, hkv):
+    """Overwrites some rows with zeros, tiny, huge, infinite and NaN values."""
+    flat = bits.reshape(-1, 128)
+    n = len(flat)
+    flat[0] = 0
+    flat[1 % n, 5] = 0x8000                      # -0
+    flat[2 % n] = 0x0001                         # the smallest subnormal
+    flat[3 % n] = 0x7F7F                         # the largest finite value
+    flat[4 % n, 127] = 0x7F80                    # +inf
+    flat[5 % n, 0] = 0xFF80                      # -inf
+    flat[6 % n, 64] = 0x7FC1                     # NaN
+    flat[7 % n] = 0x0100                         # about 2^-125: around the scale's floor
+    flat[8 % n] = np.where(np.arange(128) == 3, 0x0380, 0x0001)
+    return bits
+
+
+@pytest.mark.parametrize("hkv,T", [(2, 1), (8, 37), (32, 1000), (1, 0), (3, 517), (5, 64), (12, 41),
+                                   (256, 9), (1, 20011)])
+def test_store_is_the_definition_bit_for_bit(cuda, hkv, T):
+    rng = np.random.default_rng(T + hkv)
+    P = max(T, 64) + 100
+    kn = W.normal_bf16(rng, (T, hkv, 128))
+    vn = W.bf16_bits(rng.standard_normal((T, hkv, 128)) * np.exp(8 * rng.standard_normal((T, hkv, 1))))
+    if T >= 9:
+        _special_rows(kn, hkv)
+        _special_rows(vn[::-1], hkv)
+    slots = rng.permutation(P)[:T].astype(np.int32)
+    if T > 20:
+        slots[3], slots[11] = -1, P  # outside the pool: skipped
+    code = np.full((P, hkv, 128), 0x55, np.uint8)
+    scale = np.full((P, hkv), 7.0, np.float32)
+    want = [code.copy(), code.copy(), scale.copy(), scale.copy()]
+    ok = (slots >= 0) & (slots < P)
+    for i, new in ((0, kn), (1, vn)):
+        want[i][slots[ok]], want[2 + i][slots[ok]] = Q.quantise(new[ok])
+    dev = [torch.from_numpy(a).to(cuda) for a in (code, code, scale, scale)]
+    desc = rx.kv_desc(hkv, hkv, P, to_i32(np.zeros((1, 16), np.int32), cuda))
+    rx.store_kv_q8(desc, rx.kv_q8(*dev), to_bf16(kn, cuda), to_bf16(vn, cuda), to_i32(slots, cuda))
+    torch.cuda.synchronize()
+    for got, w in zip(dev, want):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("hkv,T", [(2, 1), (8, 37), (32, 1000), (1, 0), (3, 517), (256, 9),
+                                   (1, 20011)])
+def test_load_is_the_definition_bit_for_bit(cuda, hkv, T):
+    rng = np.random.default_rng(T + hkv)
+    P = 300
+    codes = [rng.integers(0, 254, (P, hkv, 128), dtype=np.uint8) for _ in range(2)]
+    for c in codes:
+        c[c >= 127] += 1  # every code but the NaNs (0x7f, 0xff)
+    scales = [np.exp(20 * rng.standard_normal((P, hkv))).astype(np.float32) for _ in range(2)]
+    scales[0][5], scales[1][6] = np.nan, Q.MIN_SCALE
+    slots = rng.integers(0, P, T).astype(np.int32)  # slots repeat
+    if T > 20:
+        slots[:4] = (5, 6, -1, P)
+    dev = [torch.from_numpy(a).to(cuda) for a in (*codes, *scales)]
+    desc = rx.kv_desc(hkv, hkv, P, to_i32(np.zeros((1, 16), np.int32), cuda))
+    out = [torch.full((T + 1, hkv, 128), 7.0, dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+    rx.load_kv_q8(desc, rx.kv_q8(*dev), to_i32(slots, cuda), out[0][:T], out[1][:T])
+    torch.cuda.synchronize()
+    ok = (slots >= 0) & (slots < P)
+    at = np.where(ok, slots, 0)
+    for i in range(2):
+        with np.errstate(all="ignore"):
+            x = (Q.VALUES[codes[i][at]].astype(np.float32) * scales[i][at][..., None])
+        x[~ok] = 0
+        want = torch.from_numpy(x).to(torch.bfloat16)
+        got = out[i][:T].cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want.float()))
+        assert (out[i][T] == 7).all()  # the row behind the last is left alone
+
+
+# ---- decode -----------------------------------------------------------------------------------
+
+DEC_ERR = 2.0 ** -11  # fp16 weights
+
+
+def run_decode(pool, rng, lens, group_of_req=None, group_prefix_len=None, group_parent=None,
+               q=None, stream=None):
+    B = len(lens)
+    if q is None:
+        q = W.normal_bf16(rng, (B, pool.hq, 128))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.decode_plan(plan, pool.desc, np.arange(B), lens, group_of_req, group_prefix_len,
+                   group_parent)
+    ws = workspace(plan.workspace_size(), pool.cuda)
+    ws.fill_(0xFF)  # partials that the merge reads without a write would be NaN
+    plan.upload(ws)
+    o = torch.full((B, pool.hq, 128), 7.0, dtype=torch.bfloat16, device=pool.cuda)
+    lse = torch.full((B, pool.hq), 7.0, device=pool.cuda)
+    rx.decode_attn_q8(plan, pool.desc, pool.kv, to_bf16(q, pool.cuda), o, lse, ws)
+    torch.cuda.synchronize()
+    return q, o, lse, ws, plan
+
+
+def check_decode(pool, q, o, lse, lens, pick=None):
+    for b in (range(len(lens)) if pick is None else pick):
+        pool.check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], b, lens[b],
+                   np.ones((1, lens[b]), bool), DEC_ERR, f"request {b} of {lens[b]} keys")
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (4, 4), (8, 1), (1, 1), (6, 3), (40, 5), (12, 12),
+                                    (64, 8), (16, 16), (48, 24)])
+def test_decode_own_keys(cuda, hq, hkv):
+    rng = np.random.default_rng(hq * 100 + hkv)
+    lens = [1, 2, 7, 8, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 300,
+            511, 513, 700]
+    pool = Pool(cuda, rng, hq, hkv, sum(lens) + 50, random_table(rng, sum(lens) + 50, lens))
+    q, o, lse, ws, _ = run_decode(pool, rng, lens)
+    check_decode(pool, q, o, lse, lens)
+    assert rx.read_status(ws) == rx.RX_OK
+
+
+@pytest.mark.parametrize("hq,hkv,members", [(8, 2, 4), (8, 8, 3), (8, 8, 9), (8, 8, 16), (8, 1, 2),
+                                            (16, 8, 11), (32, 8, 17), (8, 2, 40), (12, 3, 33),
+                                            (4, 1, 64), (8, 8, 130)])
+def test_decode_shared_prefixes(cuda, hq, hkv, members):
+    rng = np.random.default_rng(hq + 10 * hkv + members)
+    prefixes = (300, 33)
+    shared = {0: (list(range(members)), prefixes[0]),
+              1: (list(range(members, 2 * members)), prefixes[1])}
+    lens = [prefixes[b >= members] + int(rng.integers(0, 90)) for b in range(2 * members)] + [50, 1]
+    lens[1] = prefixes[0]  # nothing of its own
+    n = sum(prefixes) + sum(lens) + 10
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens, shared))
+    grp = [0] * members + [1] * members + [-1, -1]
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, grp, prefixes)
+    pick = None if members < 20 else [0, 1, members - 1, members, 2 * members - 1, 2 * members,
+                                      2 * members + 1, 17, 18]
+    check_decode(pool, q, o, lse, lens, pick)
+    assert rx.read_status(ws) == rx.RX_OK
+
+
+def test_decode_long_requests_split_over_many_items(cuda):
+    rng = np.random.default_rng(5)
+    lens = [20000, 3, 9001]
+    n = sum(lens) + 9
+    pool = Pool(cuda, rng, 8, 2, n, random_table(rng, n, lens))
+    q, o, lse, _, plan = run_decode(pool, rng, lens)
+    check_decode(pool, q, o, lse, lens)
+
+
+def test_decode_tree_and_grouping_give_the_same_result(cuda):
+    rng = np.random.default_rng(6)
+    lens = [500 + 7 * b for b in range(9)]
+    n = 6000
+    table = random_table(rng, n, lens)
+    table[:, :200] = table[0, :200]
+    table[:5, 200:400] = table[0, 200:400]
+    pool = Pool(cuda, rng, 16, 4, n, table)
+    args = ([1] * 5 + [0] * 4, [200, 400], [-1, 0])
+    q, o, lse, _, _ = run_decode(pool, rng, lens, *args)
+    check_decode(pool, q, o, lse, lens)
+    _, o2, lse2, _, _ = run_decode(pool, rng, lens, q=q)
+    check_decode(pool, q, o2, lse2, lens)
+
+
+def test_decode_is_the_same_on_every_call(cuda):
+    rng = np.random.default_rng(7)
+    lens = [2000, 50, 999]
+    pool = Pool(cuda, rng, 16, 2, 4000, random_table(rng, 4000, lens))
+    q, o, lse, ws, plan = run_decode(pool, rng, lens)
+    for _ in range(3):
+        o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+        rx.decode_attn_q8(plan, pool.desc, pool.kv, to_bf16(q, cuda), o2, lse2, ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_decode_scales_of_very_different_size(cuda):
+    """A key with a large score and a tiny V scale, one with a tiny score and a large V scale, zero
+    rows, and scales that grow or fall along the keys by 2^80: no weight may be lost to the fp16
+    range."""
+    rng = np.random.default_rng(8)
+    lens = [300, 300, 300, 40, 300]
+    pool = Pool(cuda, rng, 8, 8, 2000, random_table(rng, 2000, lens))
+    t = pool.table
+    pool.vs[t[0, :300]] = np.float32(2.0) ** np.linspace(-40, 40, 300)[:, None].astype(np.float32)
+    pool.vs[t[1, :300]] = np.float32(2.0) ** np.linspace(40, -40, 300)[:, None].astype(np.float32)
+    pool.ks[t[2, 7]] *= 20
+    pool.vs[t[2, 7]] = np.float32(2.0 ** -30)
+    pool.vs[t[2, 9]] = np.float32(2.0 ** 20)
+    pool.kc[t[3, :40]], pool.vc[t[3, :40]] = 0, 0
+    pool.ks[t[3, :40]] = pool.vs[t[3, :40]] = Q.MIN_SCALE
+    pool.vc[t[4, 11]], pool.vs[t[4, 11]] = 0, Q.MIN_SCALE
+    pool.ks[t[4, 11]] *= 30
+    pool.upload()
+    q, o, lse, _, _ = run_decode(pool, rng, lens)
+    check_decode(pool, q, o, lse, lens)
+
+
+def test_decode_queries_of_every_size(cuda):
+    rng = np.random.default_rng(9)
+    lens = [200] * 6
+    pool = Pool(cuda, rng, 8, 2, 1500, random_table(rng, 1500, lens))
+    x = rng.standard_normal((6, 8, 128))
+    x[0] = 0
+    x[1] *= 1e-30
+    x[2] *= 30.0
+    x[3, :, 5] = 1000.0
+    x[3, :, 6:] *= 1e-4
+    x[4] *= 2.0 ** -120
+    q, o, lse, _, _ = run_decode(pool, rng, lens, q=W.bf16_bits(x))
+    check_decode(pool, q, o, lse, lens)
+
+
+def test_decode_nan_rows_reach_their_readers_only(cuda):
+    rng = np.random.default_rng(10)
+    lens = [100, 100, 100, 260]
+    shared = {0: ([0, 1], 60)}
+    pool = Pool(cuda, rng, 8, 4, 700, random_table(rng, 700, lens, shared))
+    t = pool.table
+    spare = [s for s in range(700) if s not in set(t[:, :260].ravel().tolist())]
+    pool.ks[spare] = pool.vs[spare] = np.nan       # never read
+    clean = run_decode(pool, rng, lens, [0, 0, -1, -1], [60])
+    pool.ks[t[1, 80]] = np.nan                     # request 1's own key
+    pool.vs[t[3, 255], 2] = np.nan                 # request 3, KV head 2: V only
+    pool.upload()
+    q, o, lse, _, _ = run_decode(pool, rng, lens, [0, 0, -1, -1], [60], q=clean[0])
+    assert torch.isnan(o[1].float()).all() and torch.isnan(lse[1]).all()
+    assert torch.isnan(o[3, 4:6].float()).all() and torch.isfinite(lse[3]).all()
+    for b, rest in ((0, slice(None)), (2, slice(None)), (3, [0, 1, 2, 3, 6, 7])):
+        assert torch.equal(o[b, rest], clean[1][b, rest]) and torch.equal(lse[b], clean[2][b])
+
+
+def test_decode_entry_outside_the_pool_is_flagged_and_reads_as_zeros(cuda):
+    rng = np.random.default_rng(11)
+    lens = [90, 300]
+    for bad in (-1, 1000, 2 ** 31 - 1):
+        pool = Pool(cuda, rng, 8, 2, 1000, random_table(rng, 1000, lens))
+        pool.table[1, 133] = bad
+        pool.upload()
+        q, o, lse, ws, _ = run_decode(pool, rng, lens)
+        assert rx.read_status(ws) == rx.RX_ERR_RANGE and rx.read_status(ws) == rx.RX_OK
+        check_decode(pool, q, o, lse, lens)
+    pool.table[1, 133] = 5
+    pool.table[1, 300:] = -7  # entries past the sequence are not read
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens)
+    assert rx.read_status(ws) == rx.RX_OK
+    check_decode(pool, q, o, lse, lens)
+
+
+def test_empty_batch_launches_nothing(cuda):
+    rng = np.random.default_rng(12)
+    pool = Pool(cuda, rng, 8, 2, 64, random_table(rng, 64, [8]))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    z = np.zeros(0, np.int32)
+    rx.decode_plan(plan, pool.desc, z, z)
+    ws = workspace(plan.workspace_size(), cuda)
+    plan.upload(ws)
+    e = torch.empty((0, 8, 128), dtype=torch.bfloat16, device=cuda)
+    rx.decode_attn_q8(plan, pool.desc, pool.kv, e, e, torch.empty((0, 8), device=cuda), ws)
+    torch.cuda.synchronize()
+
+
+def test_slots_whose_offsets_pass_32_bits(cuda):
+    """A pool of more than 2^32 codes: store to, read back from and attend over its last slots."""
+    hkv, P = 32, (1 << 20) + 4096 + 7  # 4.3e9 codes in K and in V
+    rng = np.random.default_rng(13)
+    n = 200
+    slots = np.concatenate([P - 1 - rng.permutation(4000)[:n - 3], [0, 5, 9]]).astype(np.int32)
+    code = [torch.zeros((P, hkv, 128), dtype=torch.uint8, device=cuda) for _ in range(2)]
+    scale = [torch.zeros((P, hkv), device=cuda) for _ in range(2)]
+    kv = rx.kv_q8(*code, *scale)
+    r2t = to_i32(np.array([slots]), cuda)
+    desc = rx.kv_desc(hkv, hkv, P, r2t)
+    kn, vn = (W.normal_bf16(rng, (n, hkv, 128)) for _ in range(2))
+    rx.store_kv_q8(desc, kv, to_bf16(kn, cuda), to_bf16(vn, cuda), r2t[0])
+    out = [torch.empty((n, hkv, 128), dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+    rx.load_kv_q8(desc, kv, r2t[0], *out)
+    for new, got in ((kn, out[0]), (vn, out[1])):
+        c, s = Q.quantise(new)
+        want = torch.from_numpy(Q.VALUES[c].astype(np.float32) * s[..., None]).to(torch.bfloat16)
+        assert torch.equal(got.cpu(), want)
+    q = W.normal_bf16(rng, (1, hkv, 128))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.decode_plan(plan, desc, [0], [n])
+    ws = workspace(plan.workspace_size(), cuda)
+    plan.upload(ws)
+    o = torch.empty((1, hkv, 128), dtype=torch.bfloat16, device=cuda)
+    lse = torch.empty((1, hkv), device=cuda)
+    rx.decode_attn_q8(plan, desc, kv, to_bf16(q, cuda), o, lse, ws)
+    torch.cuda.synchronize()
+    (kc, ks), (vc, vs) = Q.quantise(kn), Q.quantise(vn)
+    for h in range(hkv):
+        ro, rl, pv, sabs, big = Q.attend_rows(
+            A.bf16_to_f64(q[:, h]), Q.values(kc, ks)[:, h], Q.values(vc, vs)[:, h],
+            vs[:, h].astype(np.float64), np.ones((1, n), bool), 128 ** -0.5)
+        e_s = 2.0 ** -19 * (sabs + 1)
+        tol = (2.0 ** -8 * np.abs(ro) + (DEC_ERR + 2 * e_s)[:, None] * pv * 1.01
+               + n * 2.0 ** -25 * 448 * big[:, None])
+        assert (np.abs(A.bf16_to_f64(bits_of(o[:, h])) - ro) <= tol).all()
+        assert np.abs(lse[0, h].item() - rl[0]) <= e_s[0] + 2.0 ** -22 * abs(rl[0])
+
+
+def test_two_streams_and_a_captured_graph(cuda):
+    """Plans of their own on two streams at once, and a store plus decode captured and replayed on
+    inputs that change between the replays."""
+    rng = np.random.default_rng(14)
+    lens = [700, 64, 1]
+    pool = Pool(cuda, rng, 16, 4, 2000, random_table(rng, 2000, lens))
+    q = W.normal_bf16(rng, (2, 3, 16, 128))
+    work = []
+    for i in range(2):
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        rx.decode_plan(plan, pool.desc, np.arange(3), lens)
+        ws = workspace(plan.workspace_size(), cuda)
+        plan.upload(ws)
+        work.append((plan, ws, to_bf16(q[i], cuda),
+                     torch.empty((3, 16, 128), dtype=torch.bfloat16, device=cuda),
+                     torch.empty((3, 16), device=cuda), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for plan, ws, dq, o, lse, s in work:
+            rx.decode_attn_q8(plan, pool.desc, pool.kv, dq, o, lse, ws, stream=s)
+    torch.cuda.synchronize()
+    for i, (plan, ws, dq, o, lse, s) in enumerate(work):
+        check_decode(pool, q[i], o, lse, lens)
+
+    plan, ws, dq, o, lse, _ = work[0]
+    new = [W.normal_bf16(rng, (3, 4, 128)) for _ in range(4)]
+    slots = np.array([pool.table[b, lens[b] - 1] for b in range(3)], np.int32)
+    dk, dv, ds = to_bf16(new[0], cuda), to_bf16(new[1], cuda), to_i32(slots, cuda)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rx.store_kv_q8(pool.desc, pool.kv, dk, dv, ds)
+        rx.decode_attn_q8(plan, pool.desc, pool.kv, dq, o, lse, ws)
+    for k, v in (new[:2], new[2:]):
+        dk.copy_(to_bf16(k, cuda))
+        dv.copy_(to_bf16(v, cuda))
+        o.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        pool.kc[slots], pool.ks[slots] = Q.quantise(k)
+        pool.vc[slots], pool.vs[slots] = Q.quantise(v)
+        check_decode(pool, q[0], o, lse, lens)

@@ -1,0 +1,162 @@
+"""The 8-bit pool's host side: the oracle's codes, plans for the 8-bit pool, refusals (no GPU)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import quantised as Q
+from prefix_shared_kv_gb300 import rx, workloads as W
+
+
+def test_oracle_codes_agree_with_torch():
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(Q.VALUES, want)
+    rng = np.random.default_rng(3)
+    x = np.concatenate([rng.standard_normal(4000) * s for s in (1e-3, 0.1, 1, 30, 200)])
+    grid = np.sort(Q.VALUES[np.isfinite(Q.VALUES)])
+    x = np.concatenate([x, grid, (grid[1:] + grid[:-1]) / 2])  # every code and every tie
+    x = np.clip(x, -448, 448).astype(np.float32)
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(Q.encode(x), want)
+
+
+def test_oracle_quantise_reads_back_within_half_a_step():
+    rng = np.random.default_rng(4)
+    bits = W.normal_bf16(rng, (50, 128))
+    bits[7] = 0
+    codes, scale = Q.quantise(bits)
+    x = Q.A.bf16_to_f64(bits)
+    err = np.abs(Q.values(codes, scale) - x)
+    # half an e4m3 step: 2^-4 of the value, or half of the smallest code (2^-10) times the scale;
+    # the two float32 roundings of r and x r move a value by at most 2^-23 more
+    assert (err <= np.maximum(np.abs(x) * 2.0 ** -4, scale[:, None] * 2.0 ** -10) * (1 + 1e-6)).all()
+    assert (np.abs(Q.VALUES[codes]).max(-1)[x.any(-1)] == 448).all()
+    assert scale[7] == Q.MIN_SCALE and not codes[7].any()
+
+
+def _desc(hq=8, hkv=2, pool=4096, rows=8, stride=512):
+    return rx.KVDesc(hq, hkv, 128, 128 ** -0.5, pool, 0x1000, rows, stride)
+
+
+def _decode_plan(kv_type, desc, seq_len, **groups):
+    plan = rx.Plan()
+    plan.set_kv_type(kv_type)
+    rx.decode_plan(plan, desc, np.arange(len(seq_len)), seq_len, **groups)
+    return plan
+
+
+def test_plan_kv_type_is_checked(librx):
+    plan = rx.Plan()
+    for bad in (-1, 2, 77):
+        with pytest.raises(rx.RxError) as e:
+            plan.set_kv_type(bad)
+        assert e.value.status == rx.RX_ERR_INVALID
+    assert librx.rx_plan_set_kv_type(None, 0) == rx.RX_ERR_INVALID
+
+
+def test_calls_of_the_other_pool_type_are_refused(librx):
+    desc, kv = _desc(), rx.KVQ8(4096, 4096, 4096, 4096)
+    bf, q8 = _decode_plan(rx.RX_KV_BF16, desc, [5, 9]), _decode_plan(rx.RX_KV_E4M3, desc, [5, 9])
+    q8.set_kv_type(rx.RX_KV_BF16)  # for plans built from now on: the built one stays 8-bit
+    with pytest.raises(rx.RxError) as e:
+        rx.decode_attn_q8(bf, desc, kv, 4096, 4096, 4096, 4096, stream=0)
+    assert e.value.status == rx.RX_ERR_INVALID and "bf16 pool" in str(e.value)
+    for call in (rx.decode_attn, ):
+        with pytest.raises(rx.RxError) as e:
+            call(q8, desc, 4096, 4096, 4096, 4096, 4096, 4096, stream=0)
+        assert e.value.status == rx.RX_ERR_INVALID and "8-bit pool" in str(e.value)
+
+
+def test_store_and_load_refusals(librx):
+    desc = _desc()
+    good = rx.KVQ8(4096, 4096, 4096, 4096)
+
+    def store(d=desc, kv=good, k=4096, v=4096, slots=4096, n=3):
+        return librx.rx_store_kv_q8(C.byref(d) if d else None, C.byref(kv) if kv else None, k, v,
+                                    slots, n, None)
+
+    def load(d=desc, kv=good, k=4096, v=4096, slots=4096, n=3):
+        return librx.rx_load_kv_q8(C.byref(d) if d else None, C.byref(kv) if kv else None, slots,
+                                   n, k, v, None)
+
+    bad_dim = _desc()
+    bad_dim.head_dim = 64
+    for call in (store, load):
+        assert call(d=None) == rx.RX_ERR_INVALID
+        assert call(d=bad_dim) == rx.RX_ERR_UNSUPPORTED
+        assert call(kv=None) == rx.RX_ERR_INVALID
+        for i in range(4):
+            ptrs = [4096] * 4
+            ptrs[i] = 0
+            assert call(kv=rx.KVQ8(*ptrs)) == rx.RX_ERR_INVALID
+            ptrs[i] = 4096 + 4
+            assert call(kv=rx.KVQ8(*ptrs)) == rx.RX_ERR_INVALID
+        assert call(k=0) == rx.RX_ERR_INVALID
+        assert call(v=8) == rx.RX_ERR_INVALID
+        assert call(slots=0) == rx.RX_ERR_INVALID
+        assert call(n=-1) == rx.RX_ERR_INVALID
+        assert call(n=1 << 31) == rx.RX_ERR_RANGE
+        assert call(n=0) == rx.RX_OK
+        assert call(n=0, kv=None, k=0, v=0, slots=0) == rx.RX_OK
+
+
+def test_kv_q8_checks_its_tensors():
+    code = torch.zeros(16, 2, 128, dtype=torch.uint8)
+    scale = torch.zeros(16, 2)
+    kv = rx.kv_q8(code, code.view(torch.float8_e4m3fn), scale, scale)
+    assert kv.k_code == code.data_ptr() and kv.v_scale == scale.data_ptr()
+    for bad in ((code.half(), code, scale, scale), (code, code[:8], scale, scale),
+                (code, code, scale.double(), scale), (code, code, scale, scale[:, :1]),
+                (code[:, :, ::2], code, scale, scale), (code[0], code[0], scale, scale),
+                (code.view(torch.int8), code, scale, scale)):
+        with pytest.raises(ValueError):
+            rx.kv_q8(*bad)
+
+
+def test_calls_check_their_tensors_against_the_pool_and_the_plan(librx):
+    desc = _desc(pool=16)
+    kv = rx.kv_q8(torch.zeros(16, 2, 128, dtype=torch.uint8),
+                  torch.zeros(16, 2, 128, dtype=torch.uint8), torch.zeros(16, 2),
+                  torch.zeros(16, 2))
+    rows = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):  # host tensors are refused before anything is launched
+        rx.store_kv_q8(desc, kv, rows, rows, slots, stream=0)
+    with pytest.raises(ValueError):
+        rx.load_kv_q8(desc, kv, slots, rows, rows, stream=0)
+    with pytest.raises(ValueError):
+        rx.store_kv_q8(desc, kv, rows[:2], rows, slots, stream=0)
+    with pytest.raises(ValueError):
+        rx.store_kv_q8(_desc(pool=17), kv, rows, rows, slots, stream=0)
+    plan = _decode_plan(rx.RX_KV_E4M3, desc, [5, 9])
+    o = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        rx.decode_attn_q8(plan, desc, kv, o[:1], o, torch.zeros(2, 8), 4096, stream=0)
+    with pytest.raises(ValueError):
+        rx.decode_attn_q8(plan, desc, kv, o, o, torch.zeros(2, 8).half(), 4096, stream=0)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (32, 32), (6, 3), (8, 1), (96, 12)])
+def test_decode_plan_for_the_8_bit_pool_reads_each_key_as_often_as_its_units(librx, hq, hkv):
+    """A group of up to 16 stacked rows reads its prefix once; each request its own keys once."""
+    gq = hq // hkv
+    members = 16 // gq
+    desc = _desc(hq, hkv, pool=1 << 20, rows=64, stride=4096)
+    seq = [700 + 13 * b for b in range(members)] + [1, 40]
+    plan = _decode_plan(rx.RX_KV_E4M3, desc, seq, group_of_req=[0] * members + [-1, -1],
+                        group_prefix_len=[700])
+    own = sum(13 * b for b in range(members)) + 41
+    assert plan.key_reads() == (700 + own) * hkv
+    assert plan.launches() == 2 and plan.rows() == members + 2
+
+
+def test_decode_plan_checks_are_those_of_the_bf16_pool(librx):
+    desc = _desc()
+    for seq in ([0], [513], [-1]):
+        with pytest.raises(rx.RxError) as e:
+            _decode_plan(rx.RX_KV_E4M3, desc, seq)
+        assert e.value.status == rx.RX_ERR_RANGE
+    empty = _decode_plan(rx.RX_KV_E4M3, desc, np.zeros(0, np.int32))
+    assert empty.launches() == 0 and empty.rows() == 0
