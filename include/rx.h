@@ -200,6 +200,16 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
                          const void* v_pool, const void* q, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, rx_stream_t stream);
 
+/* rx_extend_attn_q8 -- rx_extend_attn over an 8-bit pool, for an extend plan built for RX_KV_E4M3
+ * (the new tokens' KV stored there with rx_store_kv_q8 first):
+ *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
+ *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
+ * with fp32 sums of exact products of the codes.  Scales of keys a row does not see, NaN ones
+ * included, do not reach it.  pool_size * num_kv_heads is not limited. */
+rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
+                            const void* q, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, rx_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------------
  * Prefix trees (SGLang explainer, "RadixAttention: Radix Tree KV cache management"; SGLang paper
  * notes, Figure 9: tree-structured sharing).  Groups may form a forest: group_parent[g] is the

@@ -38,6 +38,14 @@
 // softmax warps write out the current one.
 // Every mbarrier wait is bounded (globaltimer); a timeout records RX_ERR_TIMEOUT in the
 // workspace status word and every role leaves its loop.
+//
+// The same kernel over an 8-bit pool (rx_extend_attn_q8; Tiles<true> below).  K and V are e4m3
+// codes with a float32 scale per (slot, KV head).  The codes are exact in bf16, so the products run
+// on them as they stand, and the scales are applied in fp32 by the softmax threads: s_j = ks_j
+// (q . kc_j) before the maximum, and P_j = bf16(p_j vs_j) after the sum, so neither product sees a
+// rounded K or V.  What differs: the producer warps load the codes into registers (16 bytes a
+// lane), a step of their own ahead and across items, turn them into bf16 and store them into the
+// ring themselves; the rings are four stages deep, which leaves room for an 8-step ring of scales.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -53,8 +61,10 @@ namespace rx {
 namespace {
 
 struct ExtParams {
-  const __nv_bfloat16* k_pool;
-  const __nv_bfloat16* v_pool;
+  const uint8_t* k_code;  // 8-bit pool (the bf16 pools come as tensor maps)
+  const uint8_t* v_code;
+  const float* k_scale;
+  const float* v_scale;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
@@ -81,58 +91,12 @@ constexpr int kWarpK = 8, kWarpV = kWarpK + kPW, kWarpMma = kWarpV + kPW;
 constexpr int kThreads = 32 * (kWarpMma + 2);  // softmax A, B | K producers | V producers | MMA A, B
 static_assert(kThreads == 512, "four warpgroups: the register split below assumes them");
 constexpr int kRegsLaunch = 65536 / kThreads;  // 128: what each thread is launched with
-constexpr int kRegsSoftmax = 160, kRegsOther = 96;
-static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * kRegsLaunch, "register split");
-constexpr int kStages = 5;             // K ring and V ring depth (64-key stages)
-// A producer warp fills every kPW-th stage of its ring and first waits for that stage to be
-// released.  That wait tests a phase parity, so it must never be two phases early: the warp's own
-// previous wait covered every step up to kPW + kStages before the current one, which rules that
-// out when the ring has at least kPW stages.
-static_assert(kStages >= kPW, "a producer could run two phases ahead");
 constexpr int kQHalf = 128 * 128;      // one 64-column half of a 128-row query tile: 16 KiB
 constexpr int kQTile = 2 * kQHalf;     // 32 KiB
 constexpr int kKVHalf = kN * 128;      // one 64-column half of a 64-key K or V tile: 8 KiB
 constexpr int kKVTile = 2 * kKVHalf;   // 16 KiB
-constexpr int kOffQ = 0;               // tile A, then tile B
-constexpr int kOffK = 2 * kQTile;
-constexpr int kOffV = kOffK + kStages * kKVTile;
-constexpr int kOffBar = kOffV + kStages * kKVTile;
-// Barriers (each waiter is at most one phase behind the barrier it tests):
-//   K_FULL[k] / V_FULL[k]   step landed in ring stage k (expect_tx by the producer + TMA bytes)
-//   K_FREE[k]  S_A and S_B of the step complete, K stage free  (two arrivals: a commit each)
-//   V_FREE[k]  PV_A and PV_B of the step complete, V stage free
-//   S_FULL[x][b]  S_x(t) complete in buffer b = t % 2 (phase t / 2).  The issuer commits it once
-//              per step after PV_x(t) and S_x(t+2) (S_x(t+2) only when there is such a step), so
-//              the phase of step t+1 also tells that PV_x(t-1) is complete: O_x may be rescaled.
-//   P_FULL[x][b]  P_x(t) in S buffer b = t % 2 (phase t / 2; tile x's 128 softmax threads).  One
-//              barrier per buffer: with S_x(t+1) already computed, the softmax can finish step
-//              t+1 before the issuer has taken step t, so a single barrier could run two phases
-//              ahead of the issuer; P_x(t+2) waits for S_x(t+2), which waits for P_x(t).
-//   O_DONE[x]  every MMA of tile x's item complete: O_x final for the epilogue
-//   Q_FULL[x]  tile x's query rows in shared memory (tile x's 128 softmax threads)
-//   TURN[x]    tile x's softmax may run its exponentials for the next step (128 arrivals of the
-//              other tile's softmax): A(0), B(0), A(1), B(1), ...
-//   DRAIN[x]   every MMA of issuer x complete, at the end: TMEM may be released
-// Phases count on across items.  Per item of tile x the issuer commits S_FULL[x] for steps
-// 0 .. ntiles + 1 (the last two without an MMA), so the S steps of successive items are
-// contiguous.  In an item with tile A only, issuer B releases each ring stage with a plain
-// arrival once the stage has landed.
-enum {
-  B_K_FULL = 0,
-  B_K_FREE = B_K_FULL + kStages,
-  B_V_FULL = B_K_FREE + kStages,
-  B_V_FREE = B_V_FULL + kStages,
-  B_S_FULL = B_V_FREE + kStages,  // [x][b] at B_S_FULL + 2 * x + b
-  B_P_FULL = B_S_FULL + 4,  // [x][b] at B_P_FULL + 2 * x + b
-  B_O_DONE = B_P_FULL + 4,
-  B_Q_FULL = B_O_DONE + 2,
-  B_TURN = B_Q_FULL + 2,
-  B_DRAIN = B_TURN + 2,
-  B_COUNT = B_DRAIN + 2
-};
-constexpr int kOffTmem = kOffBar + B_COUNT * 8;
-constexpr int kOffAbort = kOffTmem + 8;
-constexpr size_t kSmem = 1024 + kOffAbort + 16;
+constexpr int kScRing = 8;             // steps in the ring of scales (8-bit pool)
+constexpr int kScStep = 2 * kN * 4;    // K scales, then V scales, of a step's keys
 // TMEM columns: S buffers S_A0, S_A1, S_B0, S_B1 of 64 columns from 0 (P_x(t), 64 bf16 a row, two
 // a column, over the upper half of S_x's buffer t % 2), O_A [256,384), O_B [384,512)
 constexpr uint32_t kTmemCols = 512;
@@ -140,8 +104,6 @@ constexpr uint32_t kColO = 256;
 constexpr uint32_t kPOff = 32;
 constexpr uint64_t kWaitNs = 2000000000ull;
 __host__ __device__ constexpr uint32_t col_s_of(int x, int b) { return (uint32_t)(2 * x + b) * kN; }
-
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
 struct TileIter {
   int seg, k0;
@@ -211,6 +173,105 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
                : "memory");
 }
 
+struct Slot4 {
+  int v[4];
+};
+
+// Four e4m3 codes -> four bf16 (exact).  A code's seven magnitude bits, put under the sign of a bf16
+// four bits up, are the value times 2^-120 (the exponent biases are 7 and 127; subnormal codes give
+// subnormal bf16 numbers): one product restores it.  (The conversion instruction gives fp16 pairs
+// and shares the exponentials' pipe.)
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80),
+                                               __ushort_as_bfloat16(0x7B80));  // 2^120
+  const uint32_t t[2] = {__byte_perm(w, 0, 0x1404), __byte_perm(w, 0, 0x3424)};
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = ((t[i] >> 4) & 0x07f007f0u) | (t[i] & 0x80008000u);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  lo = r[0];
+  hi = r[1];
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void sts4(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+// Four floats as two packed pairs.
+__device__ __forceinline__ void lds16(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+
+// The roles of the kernel, over a bf16 pool or (Q8) an 8-bit one.
+template <bool Q8>
+struct Tiles {
+// registers of a softmax and of another thread (the 8-bit pool's producers hold a step's codes)
+static constexpr int kRegsSoftmax = Q8 ? 152 : 160, kRegsOther = Q8 ? 104 : 96;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * kRegsLaunch, "register split");
+static constexpr int kStages = Q8 ? 4 : 5;  // K ring and V ring depth (64-key stages)
+// A producer warp fills every kPW-th stage of its ring and first waits for that stage to be
+// released.  That wait tests a phase parity, so it must never be two phases early: the warp's own
+// previous wait covered every step up to kPW + kStages before the current one, which rules that
+// out when the ring has at least kPW stages.
+static_assert(kStages >= kPW, "a producer could run two phases ahead");
+static constexpr int kOffQ = 0;               // tile A, then tile B
+static constexpr int kOffK = 2 * kQTile;
+static constexpr int kOffV = kOffK + kStages * kKVTile;
+static constexpr int kOffSc = kOffV + kStages * kKVTile;
+static constexpr int kOffBar = kOffSc + (Q8 ? kScRing * kScStep : 0);
+// Barriers (each waiter is at most one phase behind the barrier it tests):
+//   K_FULL[k] / V_FULL[k]   step landed in ring stage k (expect_tx by the producer + TMA bytes)
+//   K_FREE[k]  S_A and S_B of the step complete, K stage free  (two arrivals: a commit each)
+//   V_FREE[k]  PV_A and PV_B of the step complete, V stage free
+//   S_FULL[x][b]  S_x(t) complete in buffer b = t % 2 (phase t / 2).  The issuer commits it once
+//              per step after PV_x(t) and S_x(t+2) (S_x(t+2) only when there is such a step), so
+//              the phase of step t+1 also tells that PV_x(t-1) is complete: O_x may be rescaled.
+//   P_FULL[x][b]  P_x(t) in S buffer b = t % 2 (phase t / 2; tile x's 128 softmax threads).  One
+//              barrier per buffer: with S_x(t+1) already computed, the softmax can finish step
+//              t+1 before the issuer has taken step t, so a single barrier could run two phases
+//              ahead of the issuer; P_x(t+2) waits for S_x(t+2), which waits for P_x(t).
+//   O_DONE[x]  every MMA of tile x's item complete: O_x final for the epilogue
+//   Q_FULL[x]  tile x's query rows in shared memory (tile x's 128 softmax threads)
+//   TURN[x]    tile x's softmax may run its exponentials for the next step (128 arrivals of the
+//              other tile's softmax): A(0), B(0), A(1), B(1), ...
+//   DRAIN[x]   every MMA of issuer x complete, at the end: TMEM may be released
+//   SC_FULL[k] (8-bit pool) the step's scales in entry k of their ring (its K producer).  Nothing
+//              releases an entry: a producer fills step u's only once K_FREE of step u - kStages
+//              has completed, i.e. S of that step in both tiles; S(t) is issued after P(t - 2)
+//              (an item's first two after its query rows, which follow the item before), so every
+//              softmax is then done with the scales of step u - kStages - 2, and the ring is
+//              deeper than that.  For the same reason no phase is tested two too early.
+// Phases count on across items.  Per item of tile x the issuer commits S_FULL[x] for steps
+// 0 .. ntiles + 1 (the last two without an MMA), so the S steps of successive items are
+// contiguous.  In an item with tile A only, issuer B releases each ring stage with a plain
+// arrival once the stage has landed.
+enum {
+  B_K_FULL = 0,
+  B_K_FREE = B_K_FULL + kStages,
+  B_V_FULL = B_K_FREE + kStages,
+  B_V_FREE = B_V_FULL + kStages,
+  B_S_FULL = B_V_FREE + kStages,  // [x][b] at B_S_FULL + 2 * x + b
+  B_P_FULL = B_S_FULL + 4,  // [x][b] at B_P_FULL + 2 * x + b
+  B_O_DONE = B_P_FULL + 4,
+  B_Q_FULL = B_O_DONE + 2,
+  B_TURN = B_Q_FULL + 2,
+  B_DRAIN = B_TURN + 2,
+  B_SC_FULL = B_DRAIN + 2,
+  B_COUNT = B_SC_FULL + (Q8 ? kScRing : 0)
+};
+static constexpr int kOffTmem = kOffBar + B_COUNT * 8;
+static constexpr int kOffAbort = kOffTmem + 8;
+static constexpr size_t kSmem = 1024 + kOffAbort + 16;
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(kScRing >= kStages + 3, "an entry could be overwritten while it is read");
 
 // Producer warp of one operand (K or V): steps t = w, w + kPW, ...  A warp has one
 // tile::gather4 in issue at a time (about a hundred cycles each), so the rate at which the rings
@@ -219,11 +280,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
 // half j / 16 of their 256-byte rows, with one tile::gather4 (32 gathers = the 64 keys' K or V);
 // it fetches those keys' table entries one step of its own ahead.  Keys past the segment (or
 // flagged entries) read a row past the end of the map, which the TMA fills with zeros.
-struct Slot4 {
-  int v[4];
-};
-
-__device__ __forceinline__ void producer(const ExtParams& p, int w, uint32_t base,
+static __device__ __forceinline__ void producer(const ExtParams& p, int w, uint32_t base,
                                          const CUtensorMap* map, uint32_t ring, int b_full,
                                          int b_free, volatile int* abort) {
   const int lane = threadIdx.x & 31;
@@ -273,6 +330,127 @@ __device__ __forceinline__ void producer(const ExtParams& p, int w, uint32_t bas
   }
 }
 
+// Producer warp of one operand of an 8-bit pool: the same ring steps w, w + kPW, ... of the CTA.
+// A warp holds one step's codes in registers: loaded when the step before has been stored (the
+// table entries they need were fetched a step earlier still), across item boundaries, so both
+// loads have the time of kPW ring steps to arrive.  Four lanes read 64 bytes of a row each; a
+// quarter warp stores chunks of equal parity of two neighbouring rows in one 64-column half, which
+// the 128-byte swizzle puts into different banks.  The K warps bring the scales of K and of V.
+static __device__ __forceinline__ void producer_q8(const ExtParams& p, int w, uint32_t base,
+                                                   bool is_k, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  const int sub = ((lane >> 2) & 1) + 2 * (lane >> 4);       // row of each group of four
+  const int c16 = (lane & 3) + 4 * ((lane >> 3) & 1);        // 16 codes: columns 16 c16 ..
+  const uint32_t bar = base + kOffBar;
+  const uint32_t ring = base + (is_k ? kOffK : kOffV);
+  const int b_full = is_k ? B_K_FULL : B_V_FULL, b_free = is_k ? B_K_FREE : B_V_FREE;
+  const uint8_t* codes = is_k ? p.k_code : p.v_code;
+
+  // cursor: the step whose table entries are fetched next
+  int ri = -1, n_steps = 0, n_seg = 0, t = 0, head = 0;
+  const ExtSeg* segs = nullptr;
+  TileIter at{0, 0};
+  auto advance = [&](int n) {  // n steps on; false past the last item
+    while (t + n >= n_steps) {
+      n -= n_steps - t;
+      t = 0;
+      const int idx = item_at(p, ++ri);
+      if (idx < 0) return false;
+      const ExtItem& it = p.items[idx];
+      n_steps = it.n_steps;
+      n_seg = it.n_seg;
+      head = it.kv_head;
+      segs = p.segs + it.seg_begin;
+      at = TileIter{0, n_steps > 0 ? segs[0].k_begin : 0};
+    }
+    for (int i = 0; i < n; ++i) tile_next(at, segs, n_seg);
+    t += n;
+    return true;
+  };
+  constexpr int kNoKey = INT32_MIN;  // past the segment: zeros, and no error
+  int sl[2], sl_head = 0;
+  auto fetch = [&]() {
+    const ExtSeg& sg = segs[at.seg];
+    const int32_t* row = p.req_to_token + (int64_t)sg.kv_row * p.stride;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int kpos = at.k0 + lane + 32 * j;
+      sl[j] = kpos < sg.k_end ? __ldg(row + kpos) : kNoKey;
+    }
+    sl_head = head;
+  };
+  uint4 x[16];
+  float sc[2][2] = {};
+  auto load = [&]() {  // the codes (and scales) of the step whose entries are in sl
+    int s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s[j] = sl[j];
+      if (s[j] < 0 || s[j] >= p.pool_size) {
+        if (s[j] != kNoKey) atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
+        s[j] = -1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int slot = __shfl_sync(0xffffffffu, s[i >> 3], 4 * (i & 7) + sub);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (slot >= 0)
+        x[i] = __ldg(reinterpret_cast<const uint4*>(
+            codes + ((int64_t)slot * p.hkv + sl_head) * kHeadDim + 16 * c16));
+    }
+    if (is_k) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t r = (int64_t)s[j] * p.hkv + sl_head;
+        sc[j][0] = s[j] >= 0 ? __ldg(p.k_scale + r) : 0.f;
+        sc[j][1] = s[j] >= 0 ? __ldg(p.v_scale + r) : 0.f;
+      }
+    }
+  };
+  if (!advance(w)) return;
+  fetch();
+  load();
+  bool more = advance(kPW);
+  if (more) fetch();
+  for (uint32_t gt = w;; gt += kPW) {
+    const int st = gt % kStages;
+    const bool waited = gt < kStages || tc::mbar_wait(bar + 8 * (b_free + st),
+                                                      (gt / kStages - 1) & 1, abort, p.status,
+                                                      kWaitNs);
+    if (__any_sync(0xffffffffu, !waited)) return;  // the warp leaves together
+    const uint32_t dst = ring + st * kKVTile;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t y[8];
+      e4m3x4_to_bf16(x[i].x, y[0], y[1]);
+      e4m3x4_to_bf16(x[i].y, y[2], y[3]);
+      e4m3x4_to_bf16(x[i].z, y[4], y[5]);
+      e4m3x4_to_bf16(x[i].w, y[6], y[7]);
+      sts16(dst + tile_off(4 * i + sub, 2 * c16, kKVHalf), y[0], y[1], y[2], y[3]);
+      sts16(dst + tile_off(4 * i + sub, 2 * c16 + 1, kKVHalf), y[4], y[5], y[6], y[7]);
+    }
+    if (is_k) {
+      const uint32_t e = base + kOffSc + (gt % kScRing) * kScStep + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sts4(e + 128 * j, sc[j][0]);
+        sts4(e + 128 * j + 4 * kN, sc[j][1]);
+      }
+    }
+    tc::fence_proxy_async();  // the tensor core reads what the lanes stored
+    __syncwarp();
+    if (lane == 0) {
+      if (is_k) tc::mbar_arrive(bar + 8 * (B_SC_FULL + gt % kScRing));
+      tc::mbar_arrive(bar + 8 * (b_full + st));
+    }
+    if (!more) return;
+    load();
+    more = advance(kPW);
+    if (more) fetch();
+  }
+}
+
 // MMA issuer of tile x (one thread), per item: S_x(0) and S_x(1); then per step t, once P_x(t) is
 // in TMEM, PV_x(t) and S_x(t+2) right behind it (into the buffer P_x(t) sat in).  The two tiles
 // have an issuer each (the last two warps, on different SM sub-partitions); both commit to the
@@ -281,7 +459,7 @@ __device__ __forceinline__ void producer(const ExtParams& p, int w, uint32_t bas
 // barrier operation until the tensor pipe has taken the MMAs before it, so every wait comes first.
 // The S_x(0), S_x(1) of the next item go in right after PV_x of the current one's last step: the
 // tensor pipe keeps one thread's MMAs in order, so they overwrite S buffers whose P has been used.
-__device__ __forceinline__ void mma_issuer(const ExtParams& p, int x, uint32_t base,
+static __device__ __forceinline__ void mma_issuer(const ExtParams& p, int x, uint32_t base,
                                            uint32_t tmem, volatile int* abort) {
   constexpr uint32_t idS = tc::idesc_bf16(128, kN, false, false);
   constexpr uint32_t idO = tc::idesc_bf16(128, 128, false, true);
@@ -380,7 +558,7 @@ __device__ __forceinline__ void mma_issuer(const ExtParams& p, int x, uint32_t b
 // Row maximum of the 64 raw scores (three-input maxima, eight independent chains).  Masked keys
 // hold -inf, so one code path serves every step (a smaller kernel keeps the instruction cache
 // warm for all the roles that share an SM sub-partition).
-__device__ __forceinline__ float row_max(const uint32_t (&sr)[2][32]) {
+static __device__ __forceinline__ float row_max(const uint32_t (&sr)[2][32]) {
   float m[8];
 #pragma unroll
   for (int a = 0; a < 8; ++a) m[a] = __uint_as_float(sr[0][a]);
@@ -398,7 +576,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&sr)[2][32]) {
 
 // In place, on packed fp32 pairs: s_j -> s_j * scale_log2 - m (a masked key's -inf stays -inf; m
 // is finite).
-__device__ __forceinline__ void row_shift(uint32_t (&sr)[2][32], float sl2, float m) {
+static __device__ __forceinline__ void row_shift(uint32_t (&sr)[2][32], float sl2, float m) {
   const uint64_t k2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m, -m);
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -415,20 +593,44 @@ __device__ __forceinline__ void row_shift(uint32_t (&sr)[2][32], float sl2, floa
 
 // p_e = 2^x_e for the row's 64 elements (-inf gives 0), packed to bf16 pairs in pk and added into
 // two chains of packed (even, odd) partial sums.
-__device__ __forceinline__ void row_exp(const uint32_t (&sr)[2][32], uint32_t (&pk)[32],
-                                        uint64_t (&acc)[2]) {
+// With Q8 the packed values are p_e vs_e, from the step's V scales at shared address `vs`.
+static __device__ __forceinline__ void row_exp(const uint32_t (&sr)[2][32], uint32_t (&pk)[32],
+                                               uint64_t (&acc)[2], uint32_t vs) {
 #pragma unroll
   for (int e = 0; e < kN; e += 2) {
     const int q = e >> 5, j = e & 31;
-    const float p0 = fast_exp2(__uint_as_float(sr[q][j]));
-    const float p1 = fast_exp2(__uint_as_float(sr[q][j + 1]));
+    float p0 = fast_exp2(__uint_as_float(sr[q][j]));
+    float p1 = fast_exp2(__uint_as_float(sr[q][j + 1]));
     acc[(j >> 1) & 1] = f2_add(acc[(j >> 1) & 1], f2_pack(p0, p1));
+    if constexpr (Q8) {
+      uint64_t v;
+      asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(vs + 4 * e) : "memory");
+      f2_unpack(f2_mul(f2_pack(p0, p1), v), p0, p1);
+    }
     pk[e >> 1] = pack_bf16(p0, p1);
   }
 }
 
+// In place: the row's 64 raw products times the step's K scales (at shared address `ks`).
+static __device__ __forceinline__ void row_scale(uint32_t (&sr)[2][32], uint32_t ks) {
+#pragma unroll
+  for (int e = 0; e < kN; e += 4) {
+    const int q = e >> 5, j = e & 31;
+    uint64_t k[2];
+    lds16(ks + 4 * e, k[0], k[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, b;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[q][j + 2 * i]),
+                               __uint_as_float(sr[q][j + 2 * i + 1])), k[i]), a, b);
+      sr[q][j + 2 * i] = __float_as_uint(a);
+      sr[q][j + 2 * i + 1] = __float_as_uint(b);
+    }
+  }
+}
+
 // 32 bytes to global memory (the address 32-byte aligned).
-__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
+static __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
@@ -440,7 +642,7 @@ struct RowQ {
   bool valid;
 };
 
-__device__ __forceinline__ RowQ row_of(const ExtParams& p, const ExtItem& it, int x, int r) {
+static __device__ __forceinline__ RowQ row_of(const ExtParams& p, const ExtItem& it, int x, int r) {
   // (selects rather than it.n_tok[x]: indexing the item with a runtime x would put it on the stack)
   RowQ q{-2, 0, 0, it.kv_head * p.gq + (r % p.gq), false};
   if (r < (x ? it.n_tok[1] : it.n_tok[0]) * p.gq) {
@@ -455,7 +657,7 @@ __device__ __forceinline__ RowQ row_of(const ExtParams& p, const ExtItem& it, in
 
 // Starts the copy of the thread's query row into row r of the tile's Q buffer (16 chunks of 16
 // bytes; zeros for a row past the tile's rows).
-__device__ __forceinline__ void load_q(const ExtParams& p, const RowQ& q, uint32_t qb, int r) {
+static __device__ __forceinline__ void load_q(const ExtParams& p, const RowQ& q, uint32_t qb, int r) {
   const __nv_bfloat16* src = p.q + ((int64_t)q.q_row * p.hq + q.qh) * kHeadDim;
 #pragma unroll
   for (int c = 0; c < 16; ++c)
@@ -464,22 +666,26 @@ __device__ __forceinline__ void load_q(const ExtParams& p, const RowQ& q, uint32
 }
 
 // Whether tile x's softmax and issuer take part in an item (items without steps: none).
-__device__ __forceinline__ bool has_tile(const ExtItem& it, int x) {
+static __device__ __forceinline__ bool has_tile(const ExtItem& it, int x) {
   return it.n_steps > 0 && (x == 0 || it.n_tok[1] > 0);
 }
 
 // The CTA's first item from round *ri on that has tile x (-1: none); *ri is left at its round.
-__device__ __forceinline__ int first_item(const ExtParams& p, int x, int* ri) {
+// With Q8 the ring steps of the items passed over are added to *skipped.
+static __device__ __forceinline__ int first_item(const ExtParams& p, int x, int* ri,
+                                                 uint32_t* skipped) {
   for (;; ++*ri) {
     const int idx = item_at(p, *ri);
     if (idx < 0 || has_tile(p.items[idx], x)) return idx;
+    if constexpr (Q8) *skipped += p.items[idx].n_steps;
   }
 }
 
 // Running counts over the CTA's earlier items of tile x: S steps (ntiles + 2 per item), P steps,
-// exponential turns (steps of items with both tiles), items.
+// exponential turns (steps of items with both tiles), items; and (8-bit pool) ring steps of all its
+// earlier items.
 struct SmCounts {
-  uint32_t sv, pb, tb, nq;
+  uint32_t sv, pb, tb, nq, gs;
 };
 
 // The steps of one item for a softmax thread (TWO: tile B present, the tiles take turns for the
@@ -489,7 +695,7 @@ struct SmCounts {
 // of the next item's query row.  Returns false when a wait gave up (the warp then leaves
 // together).
 template <bool TWO, class Ahead, class Prefetch>
-__device__ __forceinline__ bool softmax_steps(const ExtParams& p, const ExtItem& it,
+static __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const ExtItem& it,
                                               const ExtSeg* segs, int ntiles, const RowQ& row,
                                               const SmCounts& c, uint32_t bar, uint32_t lane_t,
                                               volatile int* abort, float& m_used, float& l,
@@ -519,7 +725,16 @@ __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const ExtItem&
     uint32_t sr[2][32];
     tc::ld32(lane_t + col_s, sr[0]);
     tc::ld32(lane_t + col_s + 32, sr[1]);
+    uint32_t scales = 0;
+    if constexpr (Q8) {
+      const uint32_t e = (c.gs + t) % kScRing;
+      const bool s_ok = tc::mbar_wait(bar + 8 * (B_SC_FULL + e), ((c.gs + t) / kScRing) & 1, abort,
+                                      p.status, kWaitNs);
+      if (__any_sync(0xffffffffu, !s_ok)) return false;
+      scales = bar - kOffBar + kOffSc + e * kScStep;
+    }
     tc::wait_ld();
+    if constexpr (Q8) row_scale(sr, scales);
     if (n_ok < kN) {  // keys at n_ok and beyond are masked: -inf
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -543,7 +758,15 @@ __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const ExtItem&
     if (__any_sync(0xffffffffu, !turn)) return false;
     uint32_t pk[32];
     uint64_t acc[2] = {0ull, 0ull};
-    row_exp(sr, pk, acc);
+    row_exp(sr, pk, acc, scales + 4 * kN);
+    if constexpr (Q8) {
+      // a masked key's P is 0 whatever its V scale is (0 * NaN is not)
+      if (n_ok < kN) {
+#pragma unroll
+        for (int e = 0; e < kN; e += 2)
+          pk[e >> 1] = e + 1 < n_ok ? pk[e >> 1] : e < n_ok ? pk[e >> 1] & 0xffffu : 0u;
+      }
+    }
     if (two && (x == 0 || t + 1 < ntiles)) tc::mbar_arrive(bar + 8 * (B_TURN + 1 - x));  // other's turn
     {
       float a0, a1, b0, b1;
@@ -586,12 +809,13 @@ __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const ExtItem&
 
 // O_x / l out of TMEM: bf16 O and natural-log LSE; for decode shared-prefix units fp32 partial
 // rows and base-2 LSE for the merge (row part[x] + r of the item).
-__device__ __forceinline__ void write_rows(const ExtParams& p, int idx, const RowQ& row,
+static __device__ __forceinline__ void write_rows(const ExtParams& p, int idx, const RowQ& row,
                                            uint32_t lane_t, float m_used, float l) {
   const int x = threadIdx.x >> 7, r = threadIdx.x & 127;
   const uint32_t col_o = kColO + x * 128;
   // l = 0: no key was visible: the row is zeros, whatever O_x holds
-  const bool none = !(l > 0.f);
+  // (8-bit pool: a NaN sum, from a NaN scale, is passed on)
+  const bool none = Q8 ? l == 0.f : !(l > 0.f);
   const float inv = none ? 0.f : 1.f / l;
   const bool partial = p.part_o != nullptr;
   int64_t prow = 0;
@@ -635,7 +859,7 @@ __device__ __forceinline__ void write_rows(const ExtParams& p, int idx, const Ro
     }
   }
   if (!row.valid) return;
-  const float lse2 = l > 0.f ? m_used + __log2f(l) : -CUDART_INF_F;
+  const float lse2 = !none ? m_used + __log2f(l) : -CUDART_INF_F;
   if (partial)
     p.part_lse[prow] = lse2;
   else
@@ -645,7 +869,7 @@ __device__ __forceinline__ void write_rows(const ExtParams& p, int idx, const Ro
 // Softmax thread r of tile x (TMEM lane r) over the CTA's items of tile x.  The next item's
 // record is loaded when an item starts and its row at the item's first step, so neither load
 // waits at the item boundary.
-__device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, uint32_t tmem,
+static __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, uint32_t tmem,
                                              volatile int* abort) {
   const int x = threadIdx.x >> 7;
   const int r = threadIdx.x & 127;
@@ -653,8 +877,9 @@ __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, 
   const uint32_t lane_t = tmem + ((uint32_t)(32 * wq) << 16);
   const uint32_t bar = base + kOffBar;
   const uint32_t qb = base + kOffQ + x * kQTile;
+  SmCounts c{0u, 0u, 0u, 0u, 0u};
   int ri = 0;
-  int idx = first_item(p, x, &ri);
+  int idx = first_item(p, x, &ri, &c.gs);
   if (idx < 0) return;
   ExtItem it = p.items[idx];
   RowQ row = row_of(p, it, x, r);
@@ -662,7 +887,6 @@ __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, 
   cp_async_wait<0>();
   tc::fence_proxy_async();
   tc::mbar_arrive(bar + 8 * (B_Q_FULL + x));
-  SmCounts c{0u, 0u, 0u, 0u};
   for (;;) {
     const ExtSeg* segs = p.segs + it.seg_begin;
     const int ntiles = it.n_steps;
@@ -698,6 +922,7 @@ __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, 
     write_rows(p, idx, row, lane_t, m_used, l);
     c.sv += ntiles + 2;
     c.pb += ntiles;
+    if constexpr (Q8) c.gs += ntiles;
     if (two) c.tb += ntiles;
     ++c.nq;
     ++ri;
@@ -710,7 +935,7 @@ __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, 
     }
     // the next item is not one of tile x's (tile B, and an item with tile A only): find the next
     // one that is and copy its query rows in now
-    idx = first_item(p, x, &ri);
+    idx = first_item(p, x, &ri, &c.gs);
     if (idx < 0) return;
     it = p.items[idx];
     row = row_of(p, it, x, r);
@@ -721,53 +946,63 @@ __device__ __forceinline__ void softmax_role(const ExtParams& p, uint32_t base, 
   }
 }
 
+};  // struct Tiles
+
+template <bool Q8>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_tc_kernel(ExtParams p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map) {
+  using T = Tiles<Q8>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023) & ~1023u;
   uint8_t* sp = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5;
-  volatile int* abort = reinterpret_cast<volatile int*>(sp + kOffAbort);
+  volatile int* abort = reinterpret_cast<volatile int*>(sp + T::kOffAbort);
   if (threadIdx.x == 0) {
-    const uint32_t bar = base + kOffBar;
-    for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(bar + 8 * (B_K_FULL + i), 1);
-      tc::mbar_init(bar + 8 * (B_K_FREE + i), 2);
-      tc::mbar_init(bar + 8 * (B_V_FULL + i), 1);
-      tc::mbar_init(bar + 8 * (B_V_FREE + i), 2);
+    const uint32_t bar = base + T::kOffBar;
+    for (int i = 0; i < T::kStages; ++i) {
+      tc::mbar_init(bar + 8 * (T::B_K_FULL + i), 1);
+      tc::mbar_init(bar + 8 * (T::B_K_FREE + i), 2);
+      tc::mbar_init(bar + 8 * (T::B_V_FULL + i), 1);
+      tc::mbar_init(bar + 8 * (T::B_V_FREE + i), 2);
     }
     for (int i = 0; i < 4; ++i) {
-      tc::mbar_init(bar + 8 * (B_S_FULL + i), 1);
-      tc::mbar_init(bar + 8 * (B_P_FULL + i), 128);
+      tc::mbar_init(bar + 8 * (T::B_S_FULL + i), 1);
+      tc::mbar_init(bar + 8 * (T::B_P_FULL + i), 128);
     }
     for (int x = 0; x < 2; ++x) {
-      tc::mbar_init(bar + 8 * (B_O_DONE + x), 1);
-      tc::mbar_init(bar + 8 * (B_Q_FULL + x), 128);
-      tc::mbar_init(bar + 8 * (B_TURN + x), 128);
-      tc::mbar_init(bar + 8 * (B_DRAIN + x), 1);
+      tc::mbar_init(bar + 8 * (T::B_O_DONE + x), 1);
+      tc::mbar_init(bar + 8 * (T::B_Q_FULL + x), 128);
+      tc::mbar_init(bar + 8 * (T::B_TURN + x), 128);
+      tc::mbar_init(bar + 8 * (T::B_DRAIN + x), 1);
     }
+    if constexpr (Q8)
+      for (int i = 0; i < kScRing; ++i) tc::mbar_init(bar + 8 * (T::B_SC_FULL + i), 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWarpMma) tc::alloc(base + kOffTmem, kTmemCols);
+  if (warp == kWarpMma) tc::alloc(base + T::kOffTmem, kTmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sp + kOffTmem);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sp + T::kOffTmem);
 
   if (warp < kWarpK) {
-    tc::regs_inc<kRegsSoftmax>();
-    softmax_role(p, base, tmem, abort);
+    tc::regs_inc<T::kRegsSoftmax>();
+    T::softmax_role(p, base, tmem, abort);
   } else {
-    tc::regs_dec<kRegsOther>();
+    tc::regs_dec<T::kRegsOther>();
     if (warp < kWarpMma) {
       const bool k = warp < kWarpV;
-      producer(p, warp - (k ? kWarpK : kWarpV), base, k ? &k_map : &v_map,
-               base + (k ? kOffK : kOffV), k ? B_K_FULL : B_V_FULL, k ? B_K_FREE : B_V_FREE, abort);
+      const int w = warp - (k ? kWarpK : kWarpV);
+      if constexpr (Q8)
+        T::producer_q8(p, w, base, k, abort);
+      else
+        T::producer(p, w, base, k ? &k_map : &v_map, base + (k ? T::kOffK : T::kOffV),
+                    k ? T::B_K_FULL : T::B_V_FULL, k ? T::B_K_FREE : T::B_V_FREE, abort);
     } else {
-      if ((threadIdx.x & 31) == 0) mma_issuer(p, warp - kWarpMma, base, tmem, abort);
+      if ((threadIdx.x & 31) == 0) T::mma_issuer(p, warp - kWarpMma, base, tmem, abort);
       __syncwarp();
     }
   }
@@ -804,11 +1039,14 @@ int make_pool_map(CUtensorMap* map, const void* pool, const rx_kv_desc* d) {
   return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
 }
 
-int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
-                      const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
-                      int32_t n_ctas, const void* k_pool, const void* v_pool, const void* q,
-                      void* o, float* lse, float* part_o, float* part_lse, int32_t* status,
-                      void* stream) {
+namespace {
+
+template <bool Q8>
+int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
+                 const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
+                 int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
+                 const void* q, void* o, float* lse, float* part_o, float* part_lse,
+                 int32_t* status, void* stream) {
   // kernel attributes belong to the current device: set once per device (bit d of the mask)
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -820,18 +1058,20 @@ int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* r
     // that only balances when every thread starts with exactly kRegsLaunch registers (with fewer,
     // the raise would wait for registers that never come), so any other build is refused.
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, extend_tc_kernel);
+    cudaError_t e = cudaFuncGetAttributes(&fa, extend_tc_kernel<Q8>);
     if (e != cudaSuccess) return (int)e;
     if (fa.numRegs != kRegsLaunch) return (int)cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(extend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmem);
+    e = cudaFuncSetAttribute(extend_tc_kernel<Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Tiles<Q8>::kSmem);
     if (e != cudaSuccess) return (int)e;
     attr_set.fetch_or(1ull << dev);
   }
   if (n_items == 0) return 0;
   ExtParams p;
-  p.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
-  p.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
+  p.k_code = Q8 ? static_cast<const uint8_t*>(kv->k_code) : nullptr;
+  p.v_code = Q8 ? static_cast<const uint8_t*>(kv->v_code) : nullptr;
+  p.k_scale = Q8 ? kv->k_scale : nullptr;
+  p.v_scale = Q8 ? kv->v_scale : nullptr;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -848,11 +1088,14 @@ int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* r
   p.status = status;
   p.part_o = part_o;
   p.part_lse = part_lse;
-  CUtensorMap k_map, v_map;
-  int e = make_pool_map(&k_map, k_pool, d);
-  if (!e) e = make_pool_map(&v_map, v_pool, d);
-  if (e) return e;
-  p.oob_row = (int32_t)(d->pool_size * d->num_kv_heads);
+  CUtensorMap k_map{}, v_map{};
+  p.oob_row = 0;
+  if constexpr (!Q8) {
+    int e = make_pool_map(&k_map, k_pool, d);
+    if (!e) e = make_pool_map(&v_map, v_pool, d);
+    if (e) return e;
+    p.oob_row = (int32_t)(d->pool_size * d->num_kv_heads);
+  }
   p.n_items = n_items;
   p.cta_begin = cta_begin;
   p.o32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
@@ -867,13 +1110,26 @@ int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* r
     grid = n_items < n_sm ? n_items : n_sm;
   }
   if (grid <= 0) return 0;
-  extend_tc_kernel<<<grid, kThreads, kSmem, (cudaStream_t)stream>>>(p, k_map, v_map);
+  extend_tc_kernel<Q8><<<grid, kThreads, Tiles<Q8>::kSmem, (cudaStream_t)stream>>>(p, k_map, v_map);
   return (int)cudaGetLastError();
 }
 
+}  // namespace
+
+int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
+                      const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
+                      int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
+                      const void* q, void* o, float* lse, float* part_o, float* part_lse,
+                      int32_t* status, void* stream) {
+  return kv ? launch_items<true>(d, items, rows, segs, n_items, cta_begin, n_ctas, nullptr,
+                                 nullptr, kv, q, o, lse, part_o, part_lse, status, stream)
+            : launch_items<false>(d, items, rows, segs, n_items, cta_begin, n_ctas, k_pool, v_pool,
+                                  nullptr, q, o, lse, part_o, part_lse, status, stream);
+}
+
 int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
-                  const void* v_pool, const void* q, void* o, float* lse, void* ws,
-                  void* stream) {
+                  const void* v_pool, const rx_kv_q8* kv, const void* q, void* o, float* lse,
+                  void* ws, void* stream) {
   uint8_t* base = static_cast<uint8_t*>(ws);
   const ExtItem* items = reinterpret_cast<const ExtItem*>(base + h->off_items);
   const ExtRow* rows = reinterpret_cast<const ExtRow*>(base + h->off_rows);
@@ -884,7 +1140,7 @@ int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                               stream);
   return launch_attn_items(d, items, rows, segs, h->n_items,
                            reinterpret_cast<const int32_t*>(base + h->off_cta), h->n_ctas, k_pool,
-                           v_pool, q, o, lse, nullptr, nullptr, status, stream);
+                           v_pool, kv, q, o, lse, nullptr, nullptr, status, stream);
 }
 
 }  // namespace rx

@@ -203,7 +203,7 @@ rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_k
       d->req_to_token_stride != p->stride || d->pool_size != p->pool)
     return fail(RX_ERR_INVALID, "descriptor differs from the one the plan was built with");
   const PlanHeader h = p->hdr();
-  if (h.n_items > 0 || h.batch > 0) {
+  if (h.n_items > 0 || (kind == 2 && h.batch > 0)) {  // an extend plan without new tokens has no rows
     if (!k || !v || !q || !o || !lse) return fail(RX_ERR_INVALID, "NULL tensor pointer");
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(o) || !aligned16(lse))
       return fail(RX_ERR_INVALID, "tensors must be 16-byte aligned");
@@ -757,6 +757,8 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   if (num_groups > 0 && !group_prefix_len) return fail(RX_ERR_INVALID, "group_prefix_len NULL");
   st = check_tree(num_groups, group_prefix_len, group_parent);
   if (st) return st;
+  if (plan->kv_next == RX_KV_E4M3 && plan->ext_kernel == RX_EXTEND_PAIR)
+    return fail(RX_ERR_UNSUPPORTED, "the SM-pair extend kernel reads bf16 pools only");
   const int hkv = desc->num_kv_heads, gq = desc->num_q_heads / hkv;
   std::vector<int64_t> cu(batch + 1, 0);
   std::vector<int> grp(batch, -1);
@@ -1036,7 +1038,20 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
   if (desc->pool_size * desc->num_kv_heads >= (int64_t)INT32_MAX)
     return fail(RX_ERR_UNSUPPORTED, "pool_size * num_kv_heads must be < 2^31 for extend");
   const PlanHeader h = plan->hdr();
-  const int e = launch_extend(desc, &h, k_pool, v_pool, q, o, lse, workspace, stream);
+  const int e = launch_extend(desc, &h, k_pool, v_pool, nullptr, q, o, lse, workspace, stream);
+  return e ? cuda_fail(e, "extend launch") : RX_OK;
+}
+
+rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
+                            const void* q, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, rx_stream_t stream) {
+  rx_status st = check_kv_q8(kv);
+  if (st) return st;
+  st = check_plan_use(plan, 1, RX_KV_E4M3, desc, kv->k_code, kv->v_code, q, o, lse, workspace,
+                      workspace_bytes);
+  if (st) return st;
+  const PlanHeader h = plan->hdr();
+  const int e = launch_extend(desc, &h, nullptr, nullptr, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "extend launch") : RX_OK;
 }
 

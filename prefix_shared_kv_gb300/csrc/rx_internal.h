@@ -149,8 +149,8 @@ int launch_decode(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
 // The extend kernel on SM pairs over `n_items` items (one tile per CTA of a pair, kPairKeys-key
 // steps).
 int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
-                  const void* v_pool, const void* q, void* o, float* lse, void* ws,
-                  void* stream);
+                  const void* v_pool, const rx_kv_q8* kv, const void* q, void* o, float* lse,
+                  void* ws, void* stream);
 int launch_extend_pair(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                        const ExtSeg* segs, int32_t n_items, const void* k_pool,
                        const void* v_pool, const void* q, void* o, float* lse, int32_t* status,
@@ -160,14 +160,15 @@ int launch_extend_pair(const rx_kv_desc* d, const ExtItem* items, const ExtRow* 
 int make_pool_map(CUtensorMap* map, const void* pool, const rx_kv_desc* d);
 // The tensor-core attention kernel over `n_items` items of tables in device memory; with
 // part_o != nullptr every tile writes fp32 partial rows (normalised O, base-2 LSE) instead of o /
-// lse.  `status` is the plan's device status word.  With `cta_begin` (device, [n_ctas + 1]) the
+// lse.  With `kv` the keys come from that 8-bit pool (k_pool and v_pool unused).
+// `status` is the plan's device status word.  With `cta_begin` (device, [n_ctas + 1]) the
 // grid is n_ctas CTAs and CTA k runs items cta_begin[k] .. cta_begin[k + 1] - 1; with null the
 // items are dealt to one CTA per SM in snake order.
 int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                       const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
-                      int32_t n_ctas, const void* k_pool, const void* v_pool, const void* q,
-                      void* o, float* lse, float* part_o, float* part_lse, int32_t* status,
-                      void* stream);
+                      int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
+                      const void* q, void* o, float* lse, float* part_o, float* part_lse,
+                      int32_t* status, void* stream);
 
 // The plan's second stream for a decode call on the current device (created on first use); all
 // NULL when the plan's calls launch a single kernel.

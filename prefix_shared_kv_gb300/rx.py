@@ -28,7 +28,7 @@ EXPORTED = [
     "rx_plan_workspace_size", "rx_plan_upload", "rx_plan_key_reads", "rx_plan_launches",
     "rx_plan_rows",
     "rx_extend_plan",
-    "rx_extend_plan_tree", "rx_extend_attn", "rx_decode_plan", "rx_decode_plan_tree",
+    "rx_extend_plan_tree", "rx_extend_attn", "rx_extend_attn_q8", "rx_decode_plan", "rx_decode_plan_tree",
     "rx_decode_attn", "rx_decode_attn_q8", "rx_decode_attn_noalloc", "rx_noalloc_read_status",
     "rx_noalloc_scratch_bytes", "rx_read_status", "rx_selftest_wait_timeout",
     "rx_selftest_pair_mma",
@@ -102,6 +102,8 @@ def lib():
                                      C.c_int32, _I32P]),
         "rx_decode_attn": (C.c_int, [_P, C.POINTER(KVDesc), _P, _P, _P, _P, _P, _P, C.c_size_t,
                                      _P]),
+        "rx_extend_attn_q8": (C.c_int, [_P, C.POINTER(KVDesc), C.POINTER(KVQ8), _P, _P, _P, _P,
+                                        C.c_size_t, _P]),
         "rx_decode_attn_q8": (C.c_int, [_P, C.POINTER(KVDesc), C.POINTER(KVQ8), _P, _P, _P, _P,
                                         C.c_size_t, _P]),
         "rx_decode_attn_noalloc": (C.c_int, [_P, C.POINTER(KVDesc), _P, _P, _P, _P, _P, _P]),
@@ -410,6 +412,11 @@ def _attn_q8(call, plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, str
                          ("lse", lse, n, torch.float32)])
     _check(call(plan.handle, C.byref(desc), C.byref(kv), _ptr(q), _ptr(o), _ptr(lse),
                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def extend_attn_q8(plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream=None):
+    """rx_extend_attn_q8: extend over an 8-bit pool with a plan built for RX_KV_E4M3."""
+    _attn_q8(lib().rx_extend_attn_q8, plan, desc, kv, q, o, lse, workspace, stream)
 
 
 def decode_attn_q8(plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream=None):

@@ -6,8 +6,9 @@ rounding.  The weights of the decode's second product are fp16: off by 2^-11 of 
 below 2^-14 of the largest term, by 2^-25 of it.  A score is a float32 sum of exact products over
 128 values; 16 roundings of partial sums of at most S = scale * sum |q_d k_d|, each 2^-23 (the
 tensor core's accumulator truncates), move it by 2^-19 S, and the exponentials and logarithms by
-2^-19; a weight is the ratio of two such terms.  The extend's weights are bf16: 2^-9 of their value
-(round to nearest of 8 significant bits), times the V scale's own rounding, 2^-24.
+2^-19; a weight is the ratio of two such terms.  The extend's weights are bf16: 2^-8 of their value
+(8 significant bits: a value in [1, 2) has steps of 2^-7 and is off by at most half of one, 2^-8;
+1 + 2^-8 itself, a tie, is off by 2^-8 / (1 + 2^-8)), times the V scale's own rounding, 2^-24.
 """
 import numpy as np
 import pytest
@@ -436,3 +437,191 @@ def test_two_streams_and_a_captured_graph(cuda):
         pool.kc[slots], pool.ks[slots] = Q.quantise(k)
         pool.vc[slots], pool.vs[slots] = Q.quantise(v)
         check_decode(pool, q[0], o, lse, lens)
+
+
+# ---- extend -----------------------------------------------------------------------------------
+
+EXT_ERR = 2.0 ** -8 + 2.0 ** -24  # bf16 weights, the V scale's product
+
+
+def run_extend(pool, rng, prefix, new, group_of_req=None, group_prefix_len=None,
+               group_parent=None, q=None):
+    n = int(np.sum(new))
+    if q is None:
+        q = W.normal_bf16(rng, (n, pool.hq, 128))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.extend_plan(plan, pool.desc, np.arange(len(new)), prefix, new, group_of_req,
+                   group_prefix_len, group_parent)
+    ws = workspace(plan.workspace_size(), pool.cuda)
+    plan.upload(ws)
+    o = torch.full((n + 1, pool.hq, 128), 7.0, dtype=torch.bfloat16, device=pool.cuda)
+    lse = torch.full((n + 1, pool.hq), 7.0, device=pool.cuda)
+    rx.extend_attn_q8(plan, pool.desc, pool.kv, to_bf16(q, pool.cuda), o[:n], lse[:n], ws)
+    torch.cuda.synchronize()
+    assert (o[n] == 7).all() and (lse[n] == 7).all()  # the row behind the last is left alone
+    return q, o[:n], lse[:n], ws
+
+
+def check_extend(pool, q, o, lse, prefix, new, pick=None):
+    cu = np.concatenate([[0], np.cumsum(new)])
+    for r in (range(len(new)) if pick is None else pick):
+        L = prefix[r] + new[r]
+        if new[r] == 0:
+            continue
+        seen = np.arange(L)[None, :] <= (prefix[r] + np.arange(new[r]))[:, None]
+        rows = slice(int(cu[r]), int(cu[r + 1]))
+        pool.check(o[rows], lse[rows], q[rows], r, L, seen, EXT_ERR,
+                   f"request {r}: {prefix[r]} cached, {new[r]} new")
+
+
+def extend_case(cuda, seed, hq, hkv, prefix, new, groups=()):
+    """groups: (members, shared prefix) each; other requests share nothing."""
+    rng = np.random.default_rng(seed)
+    lens = [p + e for p, e in zip(prefix, new)]
+    shared = {g: (list(m), p) for g, (m, p) in enumerate(groups)}
+    n = sum(lens) + 20
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens, shared))
+    grp = np.full(len(new), -1)
+    for g, (m, p) in enumerate(groups):
+        grp[list(m)] = g
+    return rng, pool, grp, [p for _, p in groups]
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (4, 4), (8, 1), (1, 1), (6, 3), (10, 5), (24, 12)])
+def test_extend_lengths_and_heads(cuda, hq, hkv):
+    prefix = [0, 0, 1, 63, 64, 65, 127, 200, 300, 5, 0]
+    new = [1, 64, 63, 1, 65, 2, 128, 0, 17, 129, 150]
+    rng, pool, grp, gpl = extend_case(cuda, hq * 10 + hkv, hq, hkv, prefix, new)
+    q, o, lse, ws = run_extend(pool, rng, prefix, new)
+    check_extend(pool, q, o, lse, prefix, new)
+    assert rx.read_status(ws) == rx.RX_OK
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (4, 4), (8, 1)])
+def test_extend_shared_prefixes(cuda, hq, hkv):
+    prefix = [200] * 6 + [333] * 3 + [64, 0]
+    new = [1, 40, 77, 3, 130, 20, 9, 64, 50, 30, 100]
+    prefix[2], prefix[7] = 260, 400  # cached tokens of their own behind the shared prefix
+    rng, pool, grp, gpl = extend_case(cuda, 3 + hq, hq, hkv, prefix, new,
+                                      [(range(6), 200), (range(6, 9), 333)])
+    q, o, lse, ws = run_extend(pool, rng, prefix, new, grp, gpl)
+    check_extend(pool, q, o, lse, prefix, new)
+    _, o2, lse2, _ = run_extend(pool, rng, prefix, new, q=q)  # the same without the groups
+    check_extend(pool, q, o2, lse2, prefix, new)
+
+
+def test_extend_many_items_per_sm_with_one_and_two_tiles(cuda):
+    """More items than SMs, items of one tile among items of two, of few steps among many."""
+    rng = np.random.default_rng(21)
+    prefix = [int(x) for x in rng.integers(0, 500, 60)]
+    new = [int(x) for x in rng.integers(1, 300, 60)]
+    prefix[:20] = [150] * 20
+    _, pool, grp, gpl = extend_case(cuda, 22, 16, 8, prefix, new, [(range(20), 150)])
+    q, o, lse, ws = run_extend(pool, rng, prefix, new, grp, gpl)
+    assert rx.read_status(ws) == rx.RX_OK
+    check_extend(pool, q, o, lse, prefix, new, pick=[0, 7, 19, 20, 33, 41, 59])
+
+
+def test_extend_long_prefix(cuda):
+    prefix, new = [9000, 3001], [70, 5]
+    rng, pool, _, _ = extend_case(cuda, 23, 4, 1, prefix, new)
+    q, o, lse, _ = run_extend(pool, rng, prefix, new)
+    check_extend(pool, q, o, lse, prefix, new)
+
+
+def test_extend_every_code_and_scale(cuda):
+    """Codes of every value (subnormal ones too) and scales over 2^60."""
+    prefix, new = [254], [64]
+    rng, pool, _, _ = extend_case(cuda, 24, 2, 2, prefix, new)
+    at = pool.table[0, :254]
+    every = np.array([c for c in range(256) if c not in (127, 255)], np.uint8)
+    pool.vc[at] = every[(np.arange(254)[:, None, None] + np.arange(128)) % 254]
+    pool.vs[at] = np.exp2(rng.integers(-30, 30, (254, 2))).astype(np.float32)
+    pool.kc[at] = every[(np.arange(254)[:, None, None] + 3 * np.arange(128)) % 254]
+    pool.ks[at] = np.float32(1 / 448)
+    pool.upload()
+    q, o, lse, _ = run_extend(pool, rng, prefix, new)
+    check_extend(pool, q, o, lse, prefix, new)
+
+
+def test_extend_nan_rows_reach_the_rows_that_see_them_only(cuda):
+    prefix, new = [100, 100, 30], [70, 20, 40]
+    rng, pool, grp, gpl = extend_case(cuda, 25, 8, 4, prefix, new, [(range(2), 100)])
+    t = pool.table
+    used = set(t[0, :170].tolist()) | set(t[1, :120].tolist()) | set(t[2, :70].tolist())
+    spare = [s for s in range(pool.n) if s not in used]
+    pool.ks[spare] = pool.vs[spare] = np.nan
+    pool.upload()
+    q, o, lse, _ = run_extend(pool, rng, prefix, new, grp, gpl)
+    pool.ks[t[0, 130]] = np.nan         # new token 30 of request 0: rows 30 .. 69 see it
+    pool.vs[t[1, 105], 1] = np.nan      # new token 5 of request 1, KV head 1
+    pool.upload()
+    _, o2, lse2, _ = run_extend(pool, rng, prefix, new, grp, gpl, q=q)
+    assert torch.isnan(o2[30:70].float()).all() and torch.isnan(lse2[30:70]).all()
+    assert torch.isnan(o2[75:90, 2:4].float()).all() and torch.isfinite(lse2[70:90]).all()
+    same = torch.ones_like(o, dtype=torch.bool)
+    same[30:70] = False
+    same[75:90, 2:4] = False
+    assert torch.equal(o2[same], o[same])
+    assert torch.equal(lse2[:30], lse[:30]) and torch.equal(lse2[70:], lse[70:])
+
+
+def test_extend_entry_outside_the_pool_is_flagged_and_reads_as_zeros(cuda):
+    prefix, new = [150, 40], [10, 80]
+    rng, pool, _, _ = extend_case(cuda, 26, 8, 2, prefix, new)
+    for bad in (-1, -9, pool.n, 2 ** 31 - 1, -2 ** 31 + 1):
+        pool.table[0, 99], pool.table[1, 41] = bad, 3
+        pool.upload()
+        q, o, lse, ws = run_extend(pool, rng, prefix, new)
+        assert rx.read_status(ws) == rx.RX_ERR_RANGE
+        check_extend(pool, q, o, lse, prefix, new)
+
+
+def test_extend_empty_and_repeated(cuda):
+    prefix, new = [20, 30], [0, 0]
+    rng, pool, _, _ = extend_case(cuda, 27, 8, 2, prefix, new)
+    run_extend(pool, rng, prefix, new)  # no new tokens: nothing is launched
+    prefix, new = [200, 500], [90, 300]
+    rng, pool, _, _ = extend_case(cuda, 28, 8, 2, prefix, new)
+    q, o, lse, _ = run_extend(pool, rng, prefix, new)
+    for _ in range(3):
+        _, o2, lse2, _ = run_extend(pool, rng, prefix, new, q=q)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_served_batch_through_the_8_bit_pool(cuda):
+    """As a server uses the calls: a prompt is stored and extended in two chunks, then decoded token
+    by token, in one captured step at the end; each output against attention over what the pool
+    then holds, and the pool read back against its codes."""
+    rng = np.random.default_rng(29)
+    hq, hkv, n = 8, 2, 400
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, [180, 150]))
+    pool.kc[:], pool.vc[:], pool.ks[:], pool.vs[:] = 0, 0, 0, 0
+    pool.upload()
+    done = [0, 0]
+
+    def store(count):
+        at = np.concatenate([pool.table[r, done[r]:done[r] + count[r]] for r in range(2)])
+        k, v = (W.normal_bf16(rng, (len(at), hkv, 128)) for _ in range(2))
+        rx.store_kv_q8(pool.desc, pool.kv, to_bf16(k, cuda), to_bf16(v, cuda), to_i32(at, cuda))
+        pool.kc[at], pool.ks[at] = Q.quantise(k)
+        pool.vc[at], pool.vs[at] = Q.quantise(v)
+
+    for count in ([100, 40], [70, 100]):
+        store(count)
+        q, o, lse, _ = run_extend(pool, rng, list(done), count)
+        check_extend(pool, q, o, lse, list(done), count)
+        done = [d + c for d, c in zip(done, count)]
+    for _ in range(3):
+        store([1, 1])
+        done = [d + 1 for d in done]
+        q, o, lse, _, _ = run_decode(pool, rng, list(done))
+        check_decode(pool, q, o, lse, list(done))
+    at = to_i32(pool.table[0, :done[0]], cuda)
+    out = [torch.empty((done[0], hkv, 128), dtype=torch.bfloat16, device=cuda) for _ in range(2)]
+    rx.load_kv_q8(pool.desc, pool.kv, at, *out)
+    K, V, _ = pool.rows(pool.table[0, :done[0]].astype(np.int64))
+    for got, want in zip(out, (K, V)):
+        # one rounding to float32 and one to bf16
+        assert (np.abs(A.bf16_to_f64(bits_of(got)) - want) <= 2.0 ** -8 * 1.001 * np.abs(want)).all()

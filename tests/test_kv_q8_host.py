@@ -63,10 +63,30 @@ def test_calls_of_the_other_pool_type_are_refused(librx):
     with pytest.raises(rx.RxError) as e:
         rx.decode_attn_q8(bf, desc, kv, 4096, 4096, 4096, 4096, stream=0)
     assert e.value.status == rx.RX_ERR_INVALID and "bf16 pool" in str(e.value)
-    for call in (rx.decode_attn, ):
+    with pytest.raises(rx.RxError) as e:
+        rx.decode_attn(q8, desc, 4096, 4096, 4096, 4096, 4096, 4096, stream=0)
+    assert e.value.status == rx.RX_ERR_INVALID and "8-bit pool" in str(e.value)
+    for kv_type, call in ((rx.RX_KV_BF16, lambda p: rx.extend_attn_q8(
+            p, desc, kv, 4096, 4096, 4096, 4096, stream=0)), (rx.RX_KV_E4M3, lambda p: rx.extend_attn(
+            p, desc, 4096, 4096, 4096, 4096, 4096, 4096, stream=0))):
+        plan = rx.Plan()
+        plan.set_kv_type(kv_type)
+        rx.extend_plan(plan, desc, [0, 1], [5, 9], [3, 1])
         with pytest.raises(rx.RxError) as e:
-            call(q8, desc, 4096, 4096, 4096, 4096, 4096, 4096, stream=0)
-        assert e.value.status == rx.RX_ERR_INVALID and "8-bit pool" in str(e.value)
+            call(plan)
+        assert e.value.status == rx.RX_ERR_INVALID and "pool" in str(e.value)
+
+
+def test_pair_kernel_is_refused_for_the_8_bit_pool(librx):
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    plan.set_extend_kernel(rx.RX_EXTEND_PAIR)
+    with pytest.raises(rx.RxError) as e:
+        rx.extend_plan(plan, _desc(), [0], [5], [3])
+    assert e.value.status == rx.RX_ERR_UNSUPPORTED
+    plan.set_extend_kernel(rx.RX_EXTEND_TILES)
+    rx.extend_plan(plan, _desc(), [0], [5], [3])
+    assert plan.rows() == 3 and plan.launches() == 1
 
 
 def test_store_and_load_refusals(librx):
