@@ -21,8 +21,9 @@
 //   warps 8-11  gather the codes by slot with 16-byte cp.async (chunks XOR-swizzled by row) and
 //               the scales with 4-byte ones into a 3-stage ring that runs on across items; an
 //               entry outside the pool is flagged and read as zeros.
-// A persistent CTA per SM takes the items in snake order (they are sorted by falling cost).  Each
-// item leaves normalised fp32 partial rows and base-2 log-sum-exps, which a second kernel merges.
+// A persistent CTA per SM runs the list of items that the planner gave it.  Each item leaves
+// normalised fp32 partial rows and base-2 log-sum-exps, which a second kernel merges; it is
+// launched beside the first one (programmatic dependent launch) and waits there for its end.
 // Waits are bounded; one that runs out records RX_ERR_TIMEOUT and every role leaves.
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -45,7 +46,6 @@ struct Params {
   const int32_t* req_to_token;
   int64_t stride;
   int hq, hkv, gq;
-  int hb_log2;  // heads of a block: 1 << hb_log2
   float scale_log2;
   const DecItem* items;
   const int32_t* rows;
@@ -53,7 +53,7 @@ struct Params {
   float* part_lse;
   int64_t pool_size;
   int32_t* status;
-  int n_items;
+  const int32_t* cta_begin;  // per-CTA item lists: [gridDim.x + 1] starts
 };
 
 constexpr int kWarps = 8;              // consumers
@@ -67,6 +67,7 @@ constexpr int kStageBytes = 2 * kHalf + 2 * kRows * 4;
 constexpr int kStages = 3;
 constexpr int kOffBar = kStages * kStageBytes;   // full[kStages], empty[kStages], abort
 constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;
+constexpr int kNoKey = INT32_MIN;      // past an item's keys
 constexpr uint64_t kWaitNs = 2000000000ull;
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
@@ -74,87 +75,89 @@ __device__ __forceinline__ uint32_t row_off(int r, int c) {  // 16-byte chunk c 
   return (uint32_t)(r * kHeadDim + ((c ^ (r & 7)) << 4));
 }
 
-// The k-th item of a CTA (snake order), -1 past the end.
+// The k-th item of the CTA's list, -1 past its end.
 __device__ __forceinline__ int item_at(const Params& p, int k) {
-  const int G = gridDim.x;
-  const int64_t i = (int64_t)k * G + ((k & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
-  return i < p.n_items ? (int)i : -1;
-}
-
-__device__ __forceinline__ int checked(const Params& p, int slot) {
-  if (slot < 0 || slot >= p.pool_size) {
-    atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
-    return -1;
-  }
-  return slot;
+  const int i = __ldg(&p.cta_begin[blockIdx.x]) + k;
+  return i < __ldg(&p.cta_begin[blockIdx.x + 1]) ? i : -1;
 }
 
 __device__ __forceinline__ void arrive_on_copies(uint32_t mbar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
+// Producer warp w of four.  Flat row f = key * HB + head of a stage takes eight lanes, so an
+// instruction copies four rows (512 contiguous bytes where a block has four heads or more), and the
+// warps take every fourth instruction.  A lane holds the table entries of keys lane, lane + 32, ...
+// of the stage, fetched a stage ahead and checked once; the copies take them by shuffle.
+template <int HBL>
 __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
-  const int tid = threadIdx.x - 32 * kWarps;
-  const int hb = 1 << p.hb_log2;
-  const int nk = kRows >> p.hb_log2;  // keys of a stage
-  const int c = tid & 7;
-  constexpr int U = kRows * 8 / kProducers;  // 16-byte chunks of K (and of V) per thread and stage
-  uint32_t g = 0;                            // stages filled so far
+  constexpr int HB = 1 << HBL, NK = kRows / HB, S = NK / 32;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kWarps;
+  const int c = lane & 7, sub = lane >> 3;
+  uint32_t g = 0;  // stages filled so far
   for (int k = 0;; ++k) {
     const int idx = item_at(p, k);
     if (idx < 0) break;
     const DecItem it = p.items[idx];
     const int nkeys = it.k_end - it.k_begin;
     const int32_t* table = p.req_to_token + (int64_t)it.kv_row * p.stride + it.k_begin;
-    const int head0 = it.head_block << p.hb_log2;
-    auto slots_of = [&](int k0, int (&sl)[U], int (&ss)[2]) {
+    const int head0 = it.head_block * HB;
+    int nxt[S];
+    auto fetch = [&](int k0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int key = k0 + ((u * (kProducers / 8) + (tid >> 3)) >> p.hb_log2);
-        sl[u] = key < nkeys ? __ldg(table + key) : -2;
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int key = k0 + ((u * kProducers + tid) >> p.hb_log2);
-        ss[u] = key < nkeys ? __ldg(table + key) : -2;
+      for (int i = 0; i < S; ++i) {
+        const int key = k0 + 32 * i + lane;
+        nxt[i] = key < nkeys ? __ldg(table + key) : kNoKey;
       }
     };
-    int sl[U], ss[2];
-    slots_of(0, sl, ss);
-    for (int k0 = 0; k0 < nkeys; k0 += nk, ++g) {
+    fetch(0);
+    for (int k0 = 0; k0 < nkeys; k0 += NK, ++g) {
       const int st = g % kStages;
       const uint32_t full = base + kOffBar + 8 * st, empty = full + 8 * kStages;
-      if (g >= kStages && !tc::mbar_wait(empty, (g / kStages - 1) & 1, abort, p.status, kWaitNs)) {
+      int sl[S];
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        sl[i] = nxt[i];
+        if (sl[i] < 0 || sl[i] >= p.pool_size) {  // flagged, and read as zeros
+          if (sl[i] != kNoKey) atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
+          sl[i] = -1;
+        }
+      }
+      if (k0 + NK < nkeys) fetch(k0 + NK);
+      const bool ok = g < kStages ||
+                      tc::mbar_wait(empty, (g / kStages - 1) & 1, abort, p.status, kWaitNs);
+      if (__any_sync(0xffffffffu, !ok)) {
         cp_async_wait<0>();
         return;
       }
       const uint32_t kb = base + st * kStageBytes, vb = kb + kHalf, sb = kb + kOffScale;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = u * (kProducers / 8) + (tid >> 3);
-        const int h = i & (hb - 1), key = i >> p.hb_log2;
-        int s = sl[u];
-        if (s != -2) s = checked(p, s);
-        const bool ok = s >= 0;
-        const int64_t off = ok ? ((int64_t)s * p.hkv + head0 + h) * kHeadDim + 16 * c : 0;
-        // row of warp (key / 32) * hb + h: its 32 keys lie together
-        const uint32_t so = row_off((((key >> 5) << p.hb_log2) + h) * kWarpKeys + (key & 31), c);
-        cp_async16(kb + so, p.k_code + off, ok);
-        cp_async16(vb + so, p.v_code + off, ok);
+      for (int i = 0; i < kRows / 16; ++i) {
+        const int f = 16 * i + 4 * w + sub;
+        const int key = f >> HBL, h = f & (HB - 1);
+        // (16 i .. 16 i + 15 lie in one run of 32 keys: the register is known here)
+        const int slot = __shfl_sync(0xffffffffu, sl[(16 * i) >> (HBL + 5)], key & 31);
+        const int64_t off =
+            slot >= 0 ? ((int64_t)slot * p.hkv + head0 + h) * kHeadDim + 16 * c : 0;
+        const uint32_t so = row_off(((key >> 5) * HB + h) * kWarpKeys + (key & 31), c);
+        cp_async16(kb + so, p.k_code + off, slot >= 0);
+        cp_async16(vb + so, p.v_code + off, slot >= 0);
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = u * kProducers + tid;
-        const int h = i & (hb - 1), key = i >> p.hb_log2;
-        const int s = ss[u];
-        const bool ok = s >= 0 && s < p.pool_size;
-        const int64_t off = ok ? (int64_t)s * p.hkv + head0 + h : 0;
-        const uint32_t r = (((key >> 5) << p.hb_log2) + h) * kWarpKeys + (key & 31);
-        cp_async4(sb + 4 * r, p.k_scale + off, ok);
-        cp_async4(sb + 4 * (kRows + r), p.v_scale + off, ok);
+      for (int i = 0; i < kRows / 128; ++i) {  // scales, [key][head]
+        const int f = 128 * i + 32 * w + lane;
+        const int key = f >> HBL, h = f & (HB - 1);
+        int slot = 0;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+          const int x = __shfl_sync(0xffffffffu, sl[j], key & 31);
+          if (j == key >> 5) slot = x;
+        }
+        const int64_t off = slot >= 0 ? (int64_t)slot * p.hkv + head0 + h : 0;
+        cp_async4(sb + 4 * f, p.k_scale + off, slot >= 0);
+        cp_async4(sb + 4 * (kRows + f), p.v_scale + off, slot >= 0);
       }
       arrive_on_copies(full);
-      if (k0 + nk < nkeys) slots_of(k0 + nk, sl, ss);
     }
   }
   cp_async_wait<0>();
@@ -167,14 +170,14 @@ __device__ __forceinline__ float lg2(float x) {
 }
 
 // One item on a consumer warp: NT tiles of 8 query rows.  Returns false when a wait gave up.
-template <int NT>
+template <int NT, int HBL>
 __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, const uint8_t* smem,
                          uint32_t& gs, volatile int* abort) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int head = (it.head_block << p.hb_log2) + (warp & ((1 << p.hb_log2) - 1));
-  const int split = warp >> p.hb_log2;
-  const int nk = kRows >> p.hb_log2;
+  constexpr int HB = 1 << HBL, nk = kRows / HB;
+  const int head = it.head_block * HB + (warp & (HB - 1));
+  const int split = warp >> HBL;
   const int nkeys = it.k_end - it.k_begin;
   const int rows = it.n_tok * p.gq;
 
@@ -241,7 +244,7 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
       const uint32_t kb = base + st * kStageBytes + warp * kWarpKeys * kHeadDim;
       const uint32_t vb = kb + kHalf;
       const float* sc = reinterpret_cast<const float*>(smem + st * kStageBytes + kOffScale) +
-                        warp * kWarpKeys;
+                        split * kWarpKeys * HB + (warp & (HB - 1));
       float s[2][NT][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -270,8 +273,8 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int key = 16 * t + 8 * h + g;
-          const float ks = sc[key];
-          lv[t][h] = lg2(sc[kRows + key]);
+          const float ks = sc[key * HB];
+          lv[t][h] = lg2(sc[kRows + key * HB]);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -371,6 +374,7 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
   return true;
 }
 
+template <int HBL>
 __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
@@ -383,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
     *abort = 0;
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x >= 32 * kWarps) {
-    producer(p, base, abort);
+    producer<HBL>(p, base, abort);
     return;
   }
   uint32_t gs = 0;
@@ -392,35 +397,41 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
     const int idx = item_at(p, k);
     if (idx < 0) return;
     const DecItem it = p.items[idx];
-    const bool ok = it.kind == 0 ? run_item<1>(p, it, base, smem, gs, abort)
-                                 : run_item<2>(p, it, base, smem, gs, abort);
+    const bool ok = it.kind == 0 ? run_item<1, HBL>(p, it, base, smem, gs, abort)
+                                 : run_item<2, HBL>(p, it, base, smem, gs, abort);
     if (!ok) return;
   }
 }
 
-// One warp per (request, query head); lane owns 4 of the 128 columns.  lse = log2 sum 2^lse_i,
-// o = sum 2^(lse_i - lse) o_i; a partial whose log-sum-exp is NaN makes both NaN.
+// W warps per (request, query head), W from the longest list of partials: warp w takes partials
+// w, w + W, ... and a lane 4 of the 128 columns; the warps' sums meet in shared memory.
+//   lse = log2 sum 2^lse_i,   o = sum 2^(lse_i - lse) o_i;
+// a partial whose log-sum-exp is NaN makes both NaN.
 constexpr int kMergeWarps = 8;
+template <int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
     const float* __restrict__ part_o, const float* __restrict__ part_lse,
     const int32_t* __restrict__ merge_idx, const DecMergeRef* __restrict__ refs, int batch, int hq,
     int gq, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
-  const int64_t task = (int64_t)blockIdx.x * kMergeWarps + threadIdx.x / 32;
-  if (task >= (int64_t)batch * hq) return;
-  const int lane = threadIdx.x % 32;
-  const int b = (int)(task / hq), h = (int)(task % hq);
+  __shared__ float4 s_acc[kMergeWarps][32];
+  __shared__ float s_max[kMergeWarps], s_tot[kMergeWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, w = warp % W;
+  const int64_t task = (int64_t)blockIdx.x * (kMergeWarps / W) + warp / W;
+  const bool live = task < (int64_t)batch * hq;
+  const int b = live ? (int)(task / hq) : 0, h = live ? (int)(task % hq) : 0;
   const int hk = h / gq, g = h % gq;
-  const int r_begin = merge_idx[b], r_end = merge_idx[b + 1];
+  const int r_begin = merge_idx[b], n = live ? merge_idx[b + 1] - r_begin : 0;
   float mx = -CUDART_INF_F, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // per chunk of 32 partials the lanes fetch one reference and log-sum-exp each, so every weight is
-  // known before any row is read and the row reads are independent of one another
-  for (int c0 = r_begin; c0 < r_end; c0 += 32) {
-    const int i = c0 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete behind it
+  // per chunk the lanes fetch one reference and log-sum-exp each, so every weight is known before
+  // any row is read and the row reads are independent of one another
+  for (int c0 = w; c0 < n; c0 += 32 * W) {
+    const int i = c0 + W * lane;
     int64_t idx = 0;
     float li = -CUDART_INF_F;
-    if (i < r_end) {
-      const DecMergeRef rf = refs[i];
+    if (i < n) {
+      const DecMergeRef rf = refs[r_begin + i];
       idx = (int64_t)rf.part + (int64_t)hk * rf.rows_real + rf.row + g;
       li = part_lse[idx];
     }
@@ -430,8 +441,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
     const float m_new = fmaxf(mx, cm);
     const float ref = m_new == -CUDART_INF_F ? 0.f : m_new;
     const float a = fast_exp2(mx - ref);  // exp2(-inf) = 0
-    const float w = li == -CUDART_INF_F ? 0.f : fast_exp2(li - ref);
-    float ws = w;
+    const float wi = li == -CUDART_INF_F ? 0.f : fast_exp2(li - ref);
+    float ws = wi;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
     tot = tot * a + ws;
@@ -440,10 +451,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
     acc.z *= a;
     acc.w *= a;
     mx = m_new;
-    const int cnt = min(32, r_end - c0);
-#pragma unroll 4
+    const int cnt = min(32, (n - c0 + W - 1) / W);
+#pragma unroll 8
     for (int j = 0; j < cnt; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float wj = __shfl_sync(0xffffffffu, wi, j);
       const int64_t ij = __shfl_sync(0xffffffffu, idx, j);
       if (wj == 0.f) continue;  // the same for the whole warp
       const float4 v = *reinterpret_cast<const float4*>(part_o + ij * kHeadDim + lane * 4);
@@ -453,6 +464,35 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
       acc.w += wj * v.w;
     }
   }
+  if constexpr (W > 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) {
+      s_max[warp] = mx;
+      s_tot[warp] = tot;
+    }
+    __syncthreads();
+    if (w != 0) return;
+    float m = mx;
+#pragma unroll
+    for (int i = 1; i < W; ++i) m = fmaxf(m, s_max[warp + i]);
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    tot = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float f = fast_exp2(s_max[warp + i] - ref);
+      const float t = s_tot[warp + i];
+      // (a warp of NaN scores only has the maximum -inf and a NaN sum)
+      tot += s_max[warp + i] == -CUDART_INF_F ? t : t * f;
+      const float4 v = s_acc[warp + i][lane];
+      acc.x += v.x * f;
+      acc.y += v.y * f;
+      acc.z += v.z * f;
+      acc.w += v.w * f;
+    }
+    mx = m;
+  }
+  if (!live) return;
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   const uint2 packed =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -463,23 +503,48 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
                    : ((mx == -CUDART_INF_F ? 0.f : mx) + __log2f(tot)) * 0.69314718055994530942f;
 }
 
+template <int W>
+cudaError_t launch_merge(const Params& p, const uint8_t* base, const PlanHeader* h, void* o,
+                         float* lse, cudaStream_t stream) {
+  const int64_t tasks = (int64_t)h->batch * p.hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((tasks + kMergeWarps / W - 1) / (kMergeWarps / W)));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute beside = {};
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &beside;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_q8_kernel<W>, (const float*)p.part_o,
+                            (const float*)p.part_lse,
+                            reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
+                            reinterpret_cast<const DecMergeRef*>(base + h->off_merge),
+                            (int)h->batch, p.hq, p.gq, static_cast<__nv_bfloat16*>(o), lse);
+}
+
+template <int HBL>
+cudaError_t launch_partials(const Params& p, int grid, cudaStream_t stream) {
+  // kernel attributes belong to the current device: set once per device (bit d of the mask)
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!((attr_set.load() >> dev) & 1)) {
+    e = cudaFuncSetAttribute(decode_q8_kernel<HBL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set.fetch_or(1ull << dev);
+  }
+  decode_q8_kernel<HBL><<<grid, kThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
                      void* o, float* lse, void* ws, void* stream) {
-  // kernel attributes belong to the current device: set once per device (bit d of the mask)
-  static std::atomic<uint64_t> attr_set{0};
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return (int)e;
-  if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
-  if (!((attr_set.load() >> dev) & 1)) {
-    e = cudaFuncSetAttribute(decode_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return (int)e;
-    attr_set.fetch_or(1ull << dev);
-  }
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return (int)e;
   uint8_t* base = static_cast<uint8_t*>(ws);
   Params p;
   p.k_code = static_cast<const uint8_t*>(kv->k_code);
@@ -492,7 +557,6 @@ int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   p.hq = d->num_q_heads;
   p.hkv = d->num_kv_heads;
   p.gq = d->num_q_heads / d->num_kv_heads;
-  p.hb_log2 = q8_head_block_log2(d->num_kv_heads);
   p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
   p.items = reinterpret_cast<const DecItem*>(base + h->off_items);
   p.rows = reinterpret_cast<const int32_t*>(base + h->off_rows);
@@ -500,21 +564,24 @@ int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   p.part_lse = reinterpret_cast<float*>(base + h->off_part_lse);
   p.pool_size = d->pool_size;
   p.status = reinterpret_cast<int32_t*>(base + offsetof(PlanHeader, status));
-  p.n_items = h->n_items;
+  p.cta_begin = reinterpret_cast<const int32_t*>(base + h->off_cta);
   cudaStream_t s = (cudaStream_t)stream;
   if (h->n_items > 0) {
-    const int grid = h->n_items < sms ? h->n_items : sms;
-    decode_q8_kernel<<<grid, kThreads, kSmem, s>>>(p);
-    e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    switch (q8_head_block_log2(d->num_kv_heads)) {
+      case 3: e = launch_partials<3>(p, h->n_ctas, s); break;
+      case 2: e = launch_partials<2>(p, h->n_ctas, s); break;
+      case 1: e = launch_partials<1>(p, h->n_ctas, s); break;
+      default: e = launch_partials<0>(p, h->n_ctas, s); break;
+    }
     if (e != cudaSuccess) return (int)e;
   }
   if (h->batch > 0) {
-    const int64_t tasks = (int64_t)h->batch * p.hq;
-    merge_q8_kernel<<<(unsigned)((tasks + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0,
-                      s>>>(p.part_o, p.part_lse,
-                           reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
-                           reinterpret_cast<const DecMergeRef*>(base + h->off_merge), h->batch,
-                           p.hq, p.gq, static_cast<__nv_bfloat16*>(o), lse);
+    // (one partial a request and head: a single read; 8 or more: eight reads in flight per warp)
+    const cudaError_t e = h->max_refs <= 8    ? launch_merge<1>(p, base, h, o, lse, s)
+                          : h->max_refs <= 32 ? launch_merge<2>(p, base, h, o, lse, s)
+                                              : launch_merge<8>(p, base, h, o, lse, s);
+    if (e != cudaSuccess) return (int)e;
   }
   return (int)cudaGetLastError();
 }

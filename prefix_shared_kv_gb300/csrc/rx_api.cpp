@@ -522,14 +522,23 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     total += (double)(seq_len[b] - (grp[b] >= 0 ? group_prefix_len[grp[b]] : 0)) * hkv * key_bytes;
   // bytes of K/V per mma.sync item: about three items per SM, but no item under 1 MiB (smaller
   // ones spend more on their own start and partial write-out than on the read)
-  const double target = std::min(4.0 * 1048576, std::max(1048576.0, total / (3.0 * device_sms())));
+  const int sms = device_sms();
+  const double target = std::min(4.0 * 1048576, std::max(1048576.0, total / (3.0 * sms)));
 
+  // Keys per item over an 8-bit pool, in whole stages: enough items for four per SM, so that their
+  // lists come out even, but none under kQ8MinStages while there is one for every SM.
+  const int q8_nk = splits * kQ8WarpKeys;
+  int q8_chunk = q8_nk;
+  if (q8) {
+    const double stages = total / (q8_nk * q8_hb * key_bytes);
+    const double per = std::max(stages / (4.0 * sms), std::min<double>(kQ8MinStages, stages / sms));
+    q8_chunk = q8_nk * (int)std::min(4096.0, std::max(1.0, std::ceil(per)));
+  }
   auto chunks = [&](int len, int kind, std::vector<std::pair<int, int>>& out) {
     const int hb = std::min(hb_of(kind), hkv);
     const int nk = q8 ? splits * kQ8WarpKeys : kDecRows / hb_of(kind);
     int max_keys = (int)(target / (hb * key_bytes));
-    max_keys = q8 ? std::max(2 * nk, max_keys)
-                  : std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
+    max_keys = q8 ? q8_chunk : std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
     const int n = (len + max_keys - 1) / max_keys;
     int c = (len + n - 1) / n;
     c = (c + nk - 1) / nk * nk;
@@ -648,6 +657,31 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   std::stable_sort(items.begin(), items.end(),
                    [&](const DecItem& a, const DecItem& b) { return cost(a) > cost(b); });
 
+  // 8-bit pool: one list per CTA, each item (costliest first) to the list that is shortest so far
+  std::vector<int32_t> cta_begin;
+  if (q8 && !items.empty()) {
+    const int32_t G = (int32_t)std::min<int64_t>(sms, (int64_t)items.size());
+    using Slot = std::pair<int64_t, int32_t>;  // (length of the list, CTA)
+    std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>> free_at;
+    for (int32_t k = 0; k < G; ++k) free_at.push({0, k});
+    std::vector<std::vector<int32_t>> lists(G);
+    for (size_t i = 0; i < items.size(); ++i) {
+      const Slot s = free_at.top();
+      free_at.pop();
+      lists[s.second].push_back((int32_t)i);
+      const int64_t st = (items[i].k_end - items[i].k_begin + q8_nk - 1) / q8_nk;
+      free_at.push({s.first + st * kQ8StageCost + kQ8ItemCost, s.second});
+    }
+    std::vector<DecItem> by_cta;
+    by_cta.reserve(items.size());
+    cta_begin.push_back(0);
+    for (const auto& l : lists) {
+      for (int32_t i : l) by_cta.push_back(items[i]);
+      cta_begin.push_back((int32_t)by_cta.size());
+    }
+    items.swap(by_cta);
+  }
+
   std::stable_sort(xitems.begin(), xitems.end(), [](const ExtItem& a, const ExtItem& b) {
     return attn_cost(a) > attn_cost(b);
   });
@@ -659,6 +693,8 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     mref.insert(mref.end(), refs[b].begin(), refs[b].end());
   }
   midx[batch] = (int32_t)mref.size();
+  int32_t max_refs = 0;
+  for (int b = 0; b < batch; ++b) max_refs = std::max(max_refs, midx[b + 1] - midx[b]);
 
   PlanHeader h;
   std::memset(&h, 0, sizeof h);
@@ -680,6 +716,9 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   h.off_xrows = off; off = align256(off + xrows.size() * sizeof(ExtRow));
   h.off_xsegs = off; off = align256(off + xsegs.size() * sizeof(ExtSeg));
   h.n_xitems = (int32_t)xitems.size();
+  h.off_cta = off; off = align256(off + cta_begin.size() * sizeof(int32_t));
+  h.n_ctas = cta_begin.empty() ? 0 : (int32_t)cta_begin.size() - 1;
+  h.max_refs = max_refs;
   const size_t tables = off;
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
   h.off_part_lse = off; off = align256(off + (size_t)npart * 4);
@@ -694,6 +733,7 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   put(plan->blob, h.off_xitems, xitems);
   put(plan->blob, h.off_xrows, xrows);
   put(plan->blob, h.off_xsegs, xsegs);
+  put(plan->blob, h.off_cta, cta_begin);
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 2;

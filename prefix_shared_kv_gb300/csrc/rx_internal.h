@@ -54,6 +54,8 @@ constexpr size_t kDecSmemBytes = (size_t)kDecStages * kDecStageBytes + kDecMaxKe
 // A work unit's partial rows: [split][KV head][row].
 constexpr int kQ8WarpKeys = 32;
 constexpr int kQ8MaxRows = 16;
+constexpr int kQ8MinStages = 8;
+constexpr int kQ8StageCost = 2, kQ8ItemCost = 3;  // planner: an item costs as much as 1.5 stages more
 inline int q8_head_block_log2(int hkv) {
   return hkv % 8 == 0 ? 3 : hkv % 4 == 0 ? 2 : hkv % 2 == 0 ? 1 : 0;
 }
@@ -116,12 +118,15 @@ struct PlanHeader {
   int64_t off_xitems, off_xrows, off_xsegs;
   int32_t n_xitems;
   int32_t ext_kernel;    // extend plans: RX_EXTEND_TILES or RX_EXTEND_PAIR
-  // extend plans on the one-SM kernel: per-CTA item lists, int32 [n_ctas + 1] starts into the
-  // item table (which is stored CTA by CTA); n_ctas = 0 when the items are dealt in snake order
+  // extend plans on the one-SM kernel, decode plans for the 8-bit pool: per-CTA item lists, int32
+  // [n_ctas + 1] starts into the item table (which is stored CTA by CTA); n_ctas = 0 when the
+  // items are dealt in snake order
   int64_t off_cta;
   int32_t n_ctas;
   int32_t kv_type;       // RX_KV_BF16 or RX_KV_E4M3: the pool the plan's calls read
-  int64_t pad[13];
+  int32_t max_refs;      // decode plans: the most partials of a request
+  int32_t pad32;
+  int64_t pad[12];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
 

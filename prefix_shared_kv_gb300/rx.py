@@ -160,7 +160,8 @@ def _ptr(t) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: building torch's Stream object costs as much as the rest of a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -220,30 +221,35 @@ def kv_q8(k_code, v_code, k_scale, v_scale) -> KVQ8:
             raise ValueError(f"{name} is {t.dtype}: float8_e4m3fn (or uint8) codes and float32 "
                              "scales expected")
     kv = KVQ8(_ptr(k_code), _ptr(v_code), _ptr(k_scale), _ptr(v_scale))
-    kv.tensors, kv.shape = (k_code, v_code, k_scale, v_scale), shape
+    kv.tensors, kv.shape, kv.device = (k_code, v_code, k_scale, v_scale), shape, k_code.get_device()
+    if any(t.get_device() != kv.device for t in kv.tensors):
+        raise ValueError("codes and scales are on different devices")
     return kv
 
 
 def _check_q8(desc: KVDesc, kv: KVQ8, named):
-    """An 8-bit call's tensors against the descriptor: the pool's shape, and per (name, tensor,
-    elements, dtype) size, dtype, layout and device.  Raw addresses (ints) and hand-made KVQ8
-    structures are the caller's responsibility."""
+    """An 8-bit call's tensors against the descriptor: the pool's shape and device, and per (name,
+    tensor, elements, dtype) size, dtype, layout and device.  Raw addresses (ints) and hand-made
+    KVQ8 structures are the caller's responsibility."""
     import torch
-    shape = getattr(kv, "shape", None)
-    if shape is not None and shape != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
-        raise ValueError(f"the pool is {shape}, the descriptor's "
+    pool = getattr(kv, "shape", None)
+    if pool is not None and pool != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
+        raise ValueError(f"the pool is {pool}, the descriptor's "
                          f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t, n, dtype in named + [("pool", t, t.numel(), t.dtype)
-                                      for t in getattr(kv, "tensors", ())]:
-        if not isinstance(t, torch.Tensor):
+    where = kv.device if pool is not None else None
+    for name, t, n, dtype in named:
+        if type(t) is int or t is None:
             continue
         if t.numel() != n:
             raise ValueError(f"{name} holds {t.numel()} elements; {n} expected")
-        if t.dtype != dtype or not t.is_contiguous():
+        if t.dtype is not dtype or not t.is_contiguous():
             raise ValueError(f"{name}: contiguous {dtype} expected, got {t.dtype}")
-        if not t.is_cuda or t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+        if where is None:
+            where = t.get_device()
+        if t.get_device() != where or where < 0:
+            raise ValueError(f"{name} is on {t.device}, the pool on device {where}")
+    if where is not None and (where < 0 or where != torch.cuda.current_device()):
+        raise ValueError("the tensors are not on the current CUDA device")
 
 
 def store_kv_q8(desc: KVDesc, kv: KVQ8, k_new, v_new, slots, stream=None):
@@ -308,9 +314,9 @@ class Plan:
 
     def rows(self) -> int:
         """Rows of q / o / lse an attention call with the plan touches (rx_plan_rows)."""
-        n = np.zeros(1, np.int64)
-        _check(lib().rx_plan_rows(self._h, n.ctypes.data_as(_I64P)))
-        return int(n[0])
+        n = C.c_int64(0)
+        _check(lib().rx_plan_rows(self._h, C.byref(n)))
+        return n.value
 
     def launches(self) -> int:
         """Kernels one attention call with the plan launches (rx_plan_launches)."""
@@ -404,12 +410,17 @@ def decode_attn(plan: Plan, desc: KVDesc, k_pool, v_pool, q, o, lse, workspace, 
                                 _stream(stream)))
 
 
+def _numel(t) -> int:
+    return t.numel() if hasattr(t, "numel") else 0
+
+
 def _attn_q8(call, plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream):
     import torch
     n = plan.rows() * desc.num_q_heads
     _check_q8(desc, kv, [("q", q, n * desc.head_dim, torch.bfloat16),
                          ("o", o, n * desc.head_dim, torch.bfloat16),
-                         ("lse", lse, n, torch.float32)])
+                         ("lse", lse, n, torch.float32),
+                         ("workspace", workspace, _numel(workspace), torch.uint8)])
     _check(call(plan.handle, C.byref(desc), C.byref(kv), _ptr(q), _ptr(o), _ptr(lse),
                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
