@@ -358,7 +358,7 @@ int launch_decode(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
         d, reinterpret_cast<const ExtItem*>(base + h->off_xitems),
         reinterpret_cast<const ExtRow*>(base + h->off_xrows),
         reinterpret_cast<const ExtSeg*>(base + h->off_xsegs), h->n_xitems, nullptr, 0, k_pool,
-        v_pool, nullptr, q, nullptr, nullptr, p.part_o, p.part_lse, p.status, st);
+        v_pool, q, nullptr, nullptr, p.part_o, p.part_lse, p.status, st);
   };
   cudaStream_t merge_stream = s;
   if (h->n_xitems > 0 && h->n_items > 0) {

@@ -43,9 +43,11 @@
 // codes with a float32 scale per (slot, KV head).  The codes are exact in bf16, so the products run
 // on them as they stand, and the scales are applied in fp32 by the softmax threads: s_j = ks_j
 // (q . kc_j) before the maximum, and P_j = bf16(p_j vs_j) after the sum, so neither product sees a
-// rounded K or V.  What differs: the producer warps load the codes into registers (16 bytes a
-// lane), a step of their own ahead and across items, turn them into bf16 and store them into the
-// ring themselves; the rings are four stages deep, which leaves room for an 8-step ring of scales.
+// rounded K or V.  A first kernel (expand_q8_kernel) writes the plan's distinct key segments into the
+// workspace, 64 keys of one KV head at a time, as the shared-memory images of the K and the V
+// operand and the keys' scales; a key is converted once however many query tiles read it, and a
+// producer fills a ring stage with one bulk copy.  The rings are four stages deep, which leaves
+// room for an 8-step ring of scales.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -61,10 +63,7 @@ namespace rx {
 namespace {
 
 struct ExtParams {
-  const uint8_t* k_code;  // 8-bit pool (the bf16 pools come as tensor maps)
-  const uint8_t* v_code;
-  const float* k_scale;
-  const float* v_scale;
+  const uint8_t* stage;  // 8-bit pool: the expanded segments (the bf16 pools come as tensor maps)
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
@@ -91,6 +90,8 @@ constexpr int kWarpK = 8, kWarpV = kWarpK + kPW, kWarpMma = kWarpV + kPW;
 constexpr int kThreads = 32 * (kWarpMma + 2);  // softmax A, B | K producers | V producers | MMA A, B
 static_assert(kThreads == 512, "four warpgroups: the register split below assumes them");
 constexpr int kRegsLaunch = 65536 / kThreads;  // 128: what each thread is launched with
+constexpr int kRegsSoftmax = 160, kRegsOther = 96;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * kRegsLaunch, "register split");
 constexpr int kQHalf = 128 * 128;      // one 64-column half of a 128-row query tile: 16 KiB
 constexpr int kQTile = 2 * kQHalf;     // 32 KiB
 constexpr int kKVHalf = kN * 128;      // one 64-column half of a 64-key K or V tile: 8 KiB
@@ -177,34 +178,17 @@ struct Slot4 {
   int v[4];
 };
 
-// Four e4m3 codes -> four bf16 (exact).  A code's seven magnitude bits, put under the sign of a bf16
-// four bits up, are the value times 2^-120 (the exponent biases are 7 and 127; subnormal codes give
-// subnormal bf16 numbers): one product restores it.  (The conversion instruction gives fp16 pairs
-// and shares the exponentials' pipe.)
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80),
-                                               __ushort_as_bfloat16(0x7B80));  // 2^120
-  const uint32_t t[2] = {__byte_perm(w, 0, 0x1404), __byte_perm(w, 0, 0x3424)};
-  uint32_t r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = ((t[i] >> 4) & 0x07f007f0u) | (t[i] & 0x80008000u);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
-    r[i] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  lo = r[0];
-  hi = r[1];
+// `bytes` contiguous bytes (16-byte aligned, a multiple of 16) from global to shared memory,
+// counted on `mbar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(mbar)
+      : "memory");
 }
 
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                      uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
-__device__ __forceinline__ void sts4(uint32_t addr, float x) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
 // Four floats as two packed pairs.
 __device__ __forceinline__ void lds16(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
@@ -213,9 +197,6 @@ __device__ __forceinline__ void lds16(uint32_t addr, uint64_t& a, uint64_t& b) {
 // The roles of the kernel, over a bf16 pool or (Q8) an 8-bit one.
 template <bool Q8>
 struct Tiles {
-// registers of a softmax and of another thread (the 8-bit pool's producers hold a step's codes)
-static constexpr int kRegsSoftmax = Q8 ? 152 : 160, kRegsOther = Q8 ? 104 : 96;
-static_assert(2 * kRegsSoftmax + 2 * kRegsOther == 4 * kRegsLaunch, "register split");
 static constexpr int kStages = Q8 ? 4 : 5;  // K ring and V ring depth (64-key stages)
 // A producer warp fills every kPW-th stage of its ring and first waits for that stage to be
 // released.  That wait tests a phase parity, so it must never be two phases early: the warp's own
@@ -330,125 +311,51 @@ static __device__ __forceinline__ void producer(const ExtParams& p, int w, uint3
   }
 }
 
-// Producer warp of one operand of an 8-bit pool: the same ring steps w, w + kPW, ... of the CTA.
-// A warp holds one step's codes in registers: loaded when the step before has been stored (the
-// table entries they need were fetched a step earlier still), across item boundaries, so both
-// loads have the time of kPW ring steps to arrive.  Four lanes read 64 bytes of a row each; a
-// quarter warp stores chunks of equal parity of two neighbouring rows in one 64-column half, which
-// the 128-byte swizzle puts into different banks.  The K warps bring the scales of K and of V.
-static __device__ __forceinline__ void producer_q8(const ExtParams& p, int w, uint32_t base,
-                                                   bool is_k, volatile int* abort) {
-  const int lane = threadIdx.x & 31;
-  const int sub = ((lane >> 2) & 1) + 2 * (lane >> 4);       // row of each group of four
-  const int c16 = (lane & 3) + 4 * ((lane >> 3) & 1);        // 16 codes: columns 16 c16 ..
+// Producer thread of one operand of an 8-bit pool: one bulk copy per step of the CTA's items, and
+// (K) one for the keys' K and V scales each.
+static __device__ __forceinline__ void producer_q8(const ExtParams& p, uint32_t base, bool is_k,
+                                                   volatile int* abort) {
   const uint32_t bar = base + kOffBar;
   const uint32_t ring = base + (is_k ? kOffK : kOffV);
   const int b_full = is_k ? B_K_FULL : B_V_FULL, b_free = is_k ? B_K_FREE : B_V_FREE;
-  const uint8_t* codes = is_k ? p.k_code : p.v_code;
-
-  // cursor: the step whose table entries are fetched next
-  int ri = -1, n_steps = 0, n_seg = 0, t = 0, head = 0;
-  const ExtSeg* segs = nullptr;
-  TileIter at{0, 0};
-  auto advance = [&](int n) {  // n steps on; false past the last item
-    while (t + n >= n_steps) {
-      n -= n_steps - t;
-      t = 0;
-      const int idx = item_at(p, ++ri);
-      if (idx < 0) return false;
-      const ExtItem& it = p.items[idx];
-      n_steps = it.n_steps;
-      n_seg = it.n_seg;
-      head = it.kv_head;
-      segs = p.segs + it.seg_begin;
-      at = TileIter{0, n_steps > 0 ? segs[0].k_begin : 0};
-    }
-    for (int i = 0; i < n; ++i) tile_next(at, segs, n_seg);
-    t += n;
-    return true;
-  };
-  constexpr int kNoKey = INT32_MIN;  // past the segment: zeros, and no error
-  int sl[2], sl_head = 0;
-  auto fetch = [&]() {
-    const ExtSeg& sg = segs[at.seg];
-    const int32_t* row = p.req_to_token + (int64_t)sg.kv_row * p.stride;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int kpos = at.k0 + lane + 32 * j;
-      sl[j] = kpos < sg.k_end ? __ldg(row + kpos) : kNoKey;
-    }
-    sl_head = head;
-  };
-  uint4 x[16];
-  float sc[2][2] = {};
-  auto load = [&]() {  // the codes (and scales) of the step whose entries are in sl
-    int s[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[j] = sl[j];
-      if (s[j] < 0 || s[j] >= p.pool_size) {
-        if (s[j] != kNoKey) atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
-        s[j] = -1;
+  // the segments are written by the kernel before this one, which may still be running; what it
+  // wrote is read by the copy engine
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("fence.proxy.async;" ::: "memory");
+  uint32_t gt = 0;
+  bool ok = true;
+  for (int ri = 0; ok; ++ri) {
+    const int idx = item_at(p, ri);
+    if (idx < 0) break;
+    const ExtItem it = p.items[idx];
+    const ExtSeg* segs = p.segs + it.seg_begin;
+    for (int sg = 0; ok && sg < it.n_seg; ++sg) {
+      const ExtSeg seg = segs[sg];
+      const uint8_t* src = p.stage + ((int64_t)seg.kv_row * p.hkv + it.kv_head) * kQ8BlockBytes +
+                           (is_k ? 0 : kQ8BlockV);
+      for (int k0 = seg.k_begin; k0 < seg.k_end; k0 += kN, ++gt) {
+        const int st = gt % kStages;
+        ok = gt < kStages || tc::mbar_wait(bar + 8 * (b_free + st), (gt / kStages - 1) & 1, abort,
+                                           p.status, kWaitNs);
+        if (!ok) break;
+        mbar_expect_tx(bar + 8 * (b_full + st), kKVTile);
+        bulk_copy(ring + st * kKVTile, src, kKVTile, bar + 8 * (b_full + st));
+        if (is_k) {
+          const uint32_t e = gt % kScRing, sc = base + kOffSc + e * kScStep;
+          mbar_expect_tx(bar + 8 * (B_SC_FULL + e), kScStep);
+          bulk_copy(sc, src + kKVTile, 4 * kN, bar + 8 * (B_SC_FULL + e));
+          bulk_copy(sc + 4 * kN, src + kQ8BlockV + kKVTile, 4 * kN, bar + 8 * (B_SC_FULL + e));
+        }
+        src += (int64_t)p.hkv * kQ8BlockBytes;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int slot = __shfl_sync(0xffffffffu, s[i >> 3], 4 * (i & 7) + sub);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (slot >= 0)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(
-            codes + ((int64_t)slot * p.hkv + sl_head) * kHeadDim + 16 * c16));
-    }
-    if (is_k) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t r = (int64_t)s[j] * p.hkv + sl_head;
-        sc[j][0] = s[j] >= 0 ? __ldg(p.k_scale + r) : 0.f;
-        sc[j][1] = s[j] >= 0 ? __ldg(p.v_scale + r) : 0.f;
-      }
-    }
-  };
-  if (!advance(w)) return;
-  fetch();
-  load();
-  bool more = advance(kPW);
-  if (more) fetch();
-  for (uint32_t gt = w;; gt += kPW) {
-    const int st = gt % kStages;
-    const bool waited = gt < kStages || tc::mbar_wait(bar + 8 * (b_free + st),
-                                                      (gt / kStages - 1) & 1, abort, p.status,
-                                                      kWaitNs);
-    if (__any_sync(0xffffffffu, !waited)) return;  // the warp leaves together
-    const uint32_t dst = ring + st * kKVTile;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t y[8];
-      e4m3x4_to_bf16(x[i].x, y[0], y[1]);
-      e4m3x4_to_bf16(x[i].y, y[2], y[3]);
-      e4m3x4_to_bf16(x[i].z, y[4], y[5]);
-      e4m3x4_to_bf16(x[i].w, y[6], y[7]);
-      sts16(dst + tile_off(4 * i + sub, 2 * c16, kKVHalf), y[0], y[1], y[2], y[3]);
-      sts16(dst + tile_off(4 * i + sub, 2 * c16 + 1, kKVHalf), y[4], y[5], y[6], y[7]);
-    }
-    if (is_k) {
-      const uint32_t e = base + kOffSc + (gt % kScRing) * kScStep + 4 * lane;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        sts4(e + 128 * j, sc[j][0]);
-        sts4(e + 128 * j + 4 * kN, sc[j][1]);
-      }
-    }
-    tc::fence_proxy_async();  // the tensor core reads what the lanes stored
-    __syncwarp();
-    if (lane == 0) {
-      if (is_k) tc::mbar_arrive(bar + 8 * (B_SC_FULL + gt % kScRing));
-      tc::mbar_arrive(bar + 8 * (b_full + st));
-    }
-    if (!more) return;
-    load();
-    more = advance(kPW);
-    if (more) fetch();
   }
+  // after an abort the copies in flight land before the CTA's shared memory is given back
+  int no_abort = 0;
+  if (!ok)
+    for (uint32_t u = gt > kStages ? gt - kStages : 0; u < gt; ++u)
+      tc::mbar_wait(bar + 8 * (b_full + u % kStages), (u / kStages) & 1, &no_abort, p.status,
+                    kWaitNs);
 }
 
 // MMA issuer of tile x (one thread), per item: S_x(0) and S_x(1); then per step t, once P_x(t) is
@@ -596,6 +503,7 @@ static __device__ __forceinline__ void row_shift(uint32_t (&sr)[2][32], float sl
 // With Q8 the packed values are p_e vs_e, from the step's V scales at shared address `vs`.
 static __device__ __forceinline__ void row_exp(const uint32_t (&sr)[2][32], uint32_t (&pk)[32],
                                                uint64_t (&acc)[2], uint32_t vs) {
+  uint64_t v[2];
 #pragma unroll
   for (int e = 0; e < kN; e += 2) {
     const int q = e >> 5, j = e & 31;
@@ -603,9 +511,8 @@ static __device__ __forceinline__ void row_exp(const uint32_t (&sr)[2][32], uint
     float p1 = fast_exp2(__uint_as_float(sr[q][j + 1]));
     acc[(j >> 1) & 1] = f2_add(acc[(j >> 1) & 1], f2_pack(p0, p1));
     if constexpr (Q8) {
-      uint64_t v;
-      asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(vs + 4 * e) : "memory");
-      f2_unpack(f2_mul(f2_pack(p0, p1), v), p0, p1);
+      if (e % 4 == 0) lds16(vs + 4 * e, v[0], v[1]);
+      f2_unpack(f2_mul(f2_pack(p0, p1), v[(e >> 1) & 1]), p0, p1);
     }
     pk[e >> 1] = pack_bf16(p0, p1);
   }
@@ -703,7 +610,7 @@ static __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const E
   constexpr bool two = TWO;
   const int x = threadIdx.x >> 7;  // tile: 0 = A, 1 = B
   const uint32_t col_o = kColO + x * 128;
-  const float sl2 = p.scale_log2;
+  const float sl2 = Q8 ? 1.f : p.scale_log2;  // (in the expanded K scales)
   // the current key segment lives in registers; the next one's record is loaded when a segment
   // starts, so no step waits for a table read
   int seg = 0, k0 = segs[0].k_begin, k_end = segs[0].k_end, s_owner = segs[0].owner;
@@ -989,16 +896,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sp + T::kOffTmem);
 
   if (warp < kWarpK) {
-    tc::regs_inc<T::kRegsSoftmax>();
+    tc::regs_inc<kRegsSoftmax>();
     T::softmax_role(p, base, tmem, abort);
   } else {
-    tc::regs_dec<T::kRegsOther>();
+    tc::regs_dec<kRegsOther>();
     if (warp < kWarpMma) {
       const bool k = warp < kWarpV;
       const int w = warp - (k ? kWarpK : kWarpV);
-      if constexpr (Q8)
-        T::producer_q8(p, w, base, k, abort);
-      else
+      if constexpr (Q8) {
+        if (w == 0 && (threadIdx.x & 31) == 0) T::producer_q8(p, base, k, abort);
+        __syncwarp();
+      } else
         T::producer(p, w, base, k ? &k_map : &v_map, base + (k ? T::kOffK : T::kOffV),
                     k ? T::B_K_FULL : T::B_V_FULL, k ? T::B_K_FREE : T::B_V_FREE, abort);
     } else {
@@ -1044,7 +952,7 @@ namespace {
 template <bool Q8>
 int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                  const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
-                 int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
+                 int32_t n_ctas, const void* k_pool, const void* v_pool, const void* stage,
                  const void* q, void* o, float* lse, float* part_o, float* part_lse,
                  int32_t* status, void* stream) {
   // kernel attributes belong to the current device: set once per device (bit d of the mask)
@@ -1068,10 +976,7 @@ int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
   }
   if (n_items == 0) return 0;
   ExtParams p;
-  p.k_code = Q8 ? static_cast<const uint8_t*>(kv->k_code) : nullptr;
-  p.v_code = Q8 ? static_cast<const uint8_t*>(kv->v_code) : nullptr;
-  p.k_scale = Q8 ? kv->k_scale : nullptr;
-  p.v_scale = Q8 ? kv->v_scale : nullptr;
+  p.stage = static_cast<const uint8_t*>(stage);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -1110,6 +1015,19 @@ int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
     grid = n_items < n_sm ? n_items : n_sm;
   }
   if (grid <= 0) return 0;
+  if constexpr (Q8) {  // launched beside the kernel that expands the segments
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Tiles<Q8>::kSmem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute beside = {};
+    beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    beside.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &beside;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, extend_tc_kernel<Q8>, p, k_map, v_map);
+  }
   extend_tc_kernel<Q8><<<grid, kThreads, Tiles<Q8>::kSmem, (cudaStream_t)stream>>>(p, k_map, v_map);
   return (int)cudaGetLastError();
 }
@@ -1118,18 +1036,16 @@ int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
 
 int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                       const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
-                      int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
-                      const void* q, void* o, float* lse, float* part_o, float* part_lse,
-                      int32_t* status, void* stream) {
-  return kv ? launch_items<true>(d, items, rows, segs, n_items, cta_begin, n_ctas, nullptr,
-                                 nullptr, kv, q, o, lse, part_o, part_lse, status, stream)
-            : launch_items<false>(d, items, rows, segs, n_items, cta_begin, n_ctas, k_pool, v_pool,
-                                  nullptr, q, o, lse, part_o, part_lse, status, stream);
+                      int32_t n_ctas, const void* k_pool, const void* v_pool, const void* q,
+                      void* o, float* lse, float* part_o, float* part_lse, int32_t* status,
+                      void* stream) {
+  return launch_items<false>(d, items, rows, segs, n_items, cta_begin, n_ctas, k_pool, v_pool,
+                             nullptr, q, o, lse, part_o, part_lse, status, stream);
 }
 
 int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
-                  const void* v_pool, const rx_kv_q8* kv, const void* q, void* o, float* lse,
-                  void* ws, void* stream) {
+                  const void* v_pool, const void* q, void* o, float* lse, void* ws,
+                  void* stream) {
   uint8_t* base = static_cast<uint8_t*>(ws);
   const ExtItem* items = reinterpret_cast<const ExtItem*>(base + h->off_items);
   const ExtRow* rows = reinterpret_cast<const ExtRow*>(base + h->off_rows);
@@ -1140,7 +1056,23 @@ int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                               stream);
   return launch_attn_items(d, items, rows, segs, h->n_items,
                            reinterpret_cast<const int32_t*>(base + h->off_cta), h->n_ctas, k_pool,
-                           v_pool, kv, q, o, lse, nullptr, nullptr, status, stream);
+                           v_pool, q, o, lse, nullptr, nullptr, status, stream);
+}
+
+int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
+                     void* o, float* lse, void* ws, void* stream) {
+  if (h->n_items == 0) return 0;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int32_t* status = reinterpret_cast<int32_t*>(base + offsetof(PlanHeader, status));
+  const int e = launch_expand_q8(d, kv, reinterpret_cast<const Q8Tile*>(base + h->off_q8_tiles),
+                                 h->n_q8_tiles, base + h->off_q8_stage, status, stream);
+  if (e) return e;
+  return launch_items<true>(d, reinterpret_cast<const ExtItem*>(base + h->off_items),
+                            reinterpret_cast<const ExtRow*>(base + h->off_rows),
+                            reinterpret_cast<const ExtSeg*>(base + h->off_segs), h->n_items,
+                            reinterpret_cast<const int32_t*>(base + h->off_cta), h->n_ctas, nullptr,
+                            nullptr, base + h->off_q8_stage, q, o, lse, nullptr, nullptr, status,
+                            stream);
 }
 
 }  // namespace rx

@@ -163,6 +163,97 @@ __global__ void __launch_bounds__(kThreads) load_q8_kernel(
   }
 }
 
+// Four e4m3 codes -> four bf16 (exact).  A code's seven magnitude bits, put under the sign of a bf16
+// four bits up, are the value times 2^-120 (the exponent biases are 7 and 127; subnormal codes give
+// subnormal bf16 numbers): one product restores it.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
+  const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80),
+                                               __ushort_as_bfloat16(0x7B80));  // 2^120
+  const uint32_t t[2] = {__byte_perm(w, 0, 0x1404), __byte_perm(w, 0, 0x3424)};
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = ((t[i] >> 4) & 0x07f007f0u) | (t[i] & 0x80008000u);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), up);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+// The expanded segments that the tensor-core extend kernel reads (layout at Q8Tile).  One CTA per
+// tile of 64 keys and group of up to eight KV heads: a lane turns 16 codes of a row of K and of V
+// into two 16-byte chunks of the operand's image; a row's codes are read by eight neighbouring
+// lanes, neighbouring heads of a key behind one another.  Moves 128 + 256 bytes a row.
+constexpr int kExpandHeads = 8;
+__global__ void __launch_bounds__(kThreads) expand_q8_kernel(
+    const uint8_t* __restrict__ k_code, const uint8_t* __restrict__ v_code,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale,
+    const int32_t* __restrict__ req_to_token, int64_t stride, int64_t pool_size, int hkv,
+    float scale_log2, const Q8Tile* __restrict__ tiles, uint8_t* __restrict__ stage,
+    int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ int32_t s_slot[kAttnKeys];
+  const Q8Tile tile = tiles[blockIdx.x];
+  const int head0 = blockIdx.y * kExpandHeads, nh = min(kExpandHeads, hkv - head0);
+  if (threadIdx.x < kAttnKeys) {
+    int s = -1;  // past the segment, or outside the pool (flagged): zeros
+    if ((int)threadIdx.x < tile.n_keys) {
+      s = __ldg(req_to_token + (int64_t)tile.kv_row * stride + tile.k_begin + threadIdx.x);
+      if (s < 0 || s >= pool_size) {
+        atomicCAS(status, 0, (int)RX_ERR_RANGE);
+        s = -1;
+      }
+    }
+    s_slot[threadIdx.x] = s;
+  }
+  __syncthreads();
+  uint8_t* blocks = stage + ((int64_t)blockIdx.x * hkv + head0) * kQ8BlockBytes;
+  for (int i = threadIdx.x; i < kAttnKeys * nh; i += kThreads) {
+    const int key = i / nh, h = i - key * nh;
+    const int64_t row = (int64_t)s_slot[key] * hkv + head0 + h;
+    const bool ok = s_slot[key] >= 0;
+    float* sc = reinterpret_cast<float*>(blocks + (int64_t)h * kQ8BlockBytes + kQ8BlockV) -
+                kAttnKeys + key;
+    sc[0] = ok ? __ldg(k_scale + row) * scale_log2 : 0.f;
+    sc[kQ8BlockV / 4] = ok ? __ldg(v_scale + row) : 0.f;
+  }
+  const int n = kAttnKeys * nh * 8;
+  constexpr int U = 4;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    uint4 x[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        const int f = i >> 3, key = f / nh, h = f - key * nh;
+        const int slot = s_slot[key];
+        if (slot >= 0) {
+          const int64_t off = ((int64_t)slot * hkv + head0 + h) * kHeadDim + 16 * (i & 7);
+          x[u][0] = __ldg(reinterpret_cast<const uint4*>(k_code + off));
+          x[u][1] = __ldg(reinterpret_cast<const uint4*>(v_code + off));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= n) break;
+      const int c = i & 7, f = i >> 3, key = f / nh, h = f - key * nh;
+      // chunks 2c and 2c + 1 of the row: half c / 4, swizzled by the row's low three bits
+      uint8_t* dst = blocks + (int64_t)h * kQ8BlockBytes + (c >> 2) * (kAttnKeys * 128) + key * 128;
+      const int c0 = (((2 * c) & 7) ^ (key & 7)) << 4, c1 = (((2 * c + 1) & 7) ^ (key & 7)) << 4;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint2 a = e4m3x4_to_bf16(x[u][v].x), b = e4m3x4_to_bf16(x[u][v].y);
+        const uint2 e = e4m3x4_to_bf16(x[u][v].z), g = e4m3x4_to_bf16(x[u][v].w);
+        *reinterpret_cast<uint4*>(dst + v * kQ8BlockV + c0) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(dst + v * kQ8BlockV + c1) = make_uint4(e.x, e.y, g.x, g.y);
+      }
+    }
+  }
+}
+
 int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -207,6 +298,16 @@ int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* sl
     return (int)cudaGetLastError();
   };
   return run(load_q8_kernel<4>, 4);
+}
+
+int launch_expand_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const Q8Tile* tiles, int32_t n_tiles,
+                     void* stage, int32_t* status, void* stream) {
+  const dim3 grid(n_tiles, (d->num_kv_heads + kExpandHeads - 1) / kExpandHeads);
+  expand_q8_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
+      (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale,
+      d->req_to_token, d->req_to_token_stride, d->pool_size, d->num_kv_heads,
+      d->softmax_scale * 1.4426950408889634f, tiles, (uint8_t*)stage, status);
+  return (int)cudaGetLastError();
 }
 
 }  // namespace rx

@@ -371,7 +371,8 @@ rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches) {
   // the same conditions the launchers test: extend -- the tensor-core kernel when there are
   // items; decode -- the tensor-core kernel for its shared-prefix units, the mma.sync partial
   // kernel for the others, and the merge whenever there are requests
-  *launches = plan->kind == 1 ? (h.n_items > 0)
+  // (an extend over an 8-bit pool expands the plan's keys in a kernel of its own first)
+  *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3))
                               : (h.n_xitems > 0) + (h.n_items > 0) + (h.batch > 0);
   return RX_OK;
 }
@@ -1037,6 +1038,32 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     items.swap(by_cta);
   }
 
+  // 8-bit pool: each distinct segment (table row, first key) gets tiles of kAttnKeys keys, as many
+  // as its longest use needs, and the segments refer to their first tile
+  std::vector<Q8Tile> tiles8;
+  if (plan->kv_next == RX_KV_E4M3) {
+    std::unordered_map<int64_t, std::pair<int32_t, int32_t>> where;  // -> (longest end, first tile)
+    auto key_of = [](const ExtSeg& sg) { return (int64_t)sg.kv_row << 32 | (uint32_t)sg.k_begin; };
+    for (const ExtSeg& sg : segs) {
+      auto& w = where[key_of(sg)];
+      w.first = std::max(w.first, sg.k_end);
+      w.second = -1;
+    }
+    for (ExtSeg& sg : segs) {
+      auto& w = where[key_of(sg)];
+      if (w.second < 0) {
+        if ((int64_t)tiles8.size() + attn_steps(w.first - sg.k_begin) > (int64_t)INT32_MAX / 2)
+          return fail(RX_ERR_RANGE, "plan too large");
+        w.second = (int32_t)tiles8.size();
+        for (int k = sg.k_begin; k < w.first; k += kAttnKeys)
+          tiles8.push_back({sg.kv_row, k, std::min(kAttnKeys, w.first - k), 0});
+      }
+      sg.kv_row = w.second;
+    }
+    key_reads = 0;  // the pool is read by the expansion only
+    for (const Q8Tile& t : tiles8) key_reads += (int64_t)t.n_keys * hkv;
+  }
+
   PlanHeader h;
   std::memset(&h, 0, sizeof h);
   h.magic = kPlanMagic;
@@ -1054,14 +1081,18 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   h.off_segs = off; off = align256(off + segs.size() * sizeof(ExtSeg));
   h.off_cta = off; off = align256(off + cta_begin.size() * sizeof(int32_t));
   h.n_ctas = cta_begin.empty() ? 0 : (int32_t)cta_begin.size() - 1;
+  h.off_q8_tiles = off; off = align256(off + tiles8.size() * sizeof(Q8Tile));
+  h.n_q8_tiles = (int32_t)tiles8.size();
   h.off_merge_idx = h.off_merge = h.off_part_o = h.off_part_lse = off;
-  h.total_bytes = off;
   plan->blob.assign(off, 0);
+  h.off_q8_stage = off; off = align256(off + tiles8.size() * (size_t)hkv * kQ8BlockBytes);
+  h.total_bytes = off;
   std::memcpy(plan->blob.data(), &h, sizeof h);
   put(plan->blob, h.off_items, items);
   put(plan->blob, h.off_rows, rows);
   put(plan->blob, h.off_segs, segs);
   put(plan->blob, h.off_cta, cta_begin);
+  put(plan->blob, h.off_q8_tiles, tiles8);
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 1;
@@ -1078,7 +1109,7 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
   if (desc->pool_size * desc->num_kv_heads >= (int64_t)INT32_MAX)
     return fail(RX_ERR_UNSUPPORTED, "pool_size * num_kv_heads must be < 2^31 for extend");
   const PlanHeader h = plan->hdr();
-  const int e = launch_extend(desc, &h, k_pool, v_pool, nullptr, q, o, lse, workspace, stream);
+  const int e = launch_extend(desc, &h, k_pool, v_pool, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "extend launch") : RX_OK;
 }
 
@@ -1091,7 +1122,7 @@ rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const r
                       workspace_bytes);
   if (st) return st;
   const PlanHeader h = plan->hdr();
-  const int e = launch_extend(desc, &h, nullptr, nullptr, kv, q, o, lse, workspace, stream);
+  const int e = launch_extend_q8(desc, &h, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "extend launch") : RX_OK;
 }
 

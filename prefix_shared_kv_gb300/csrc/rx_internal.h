@@ -85,6 +85,21 @@ struct ExtSeg {
 constexpr int kAttnKeys = 64;
 constexpr int kPairKeys = 128;
 
+// Extend over an 8-bit pool.  The distinct key segments of the plan, in tiles of kAttnKeys keys, are
+// expanded into the workspace by a kernel of their own; ExtSeg::kv_row is then the segment's first
+// tile (its step i reads tile kv_row + i).  Block (tile, KV head), at tile * Hkv + head: the K
+// operand's shared-memory image (bf16 codes, two 64-column halves of 128-byte-swizzled rows), the
+// keys' K scales times softmax_scale * log2(e), the V operand's image, the keys' V scales.  Keys
+// past the segment are zeros with scale 0.
+struct Q8Tile {
+  int32_t kv_row;        // req_to_token row
+  int32_t k_begin;
+  int32_t n_keys;        // 1 .. kAttnKeys
+  int32_t pad;
+};
+constexpr int kQ8BlockV = kAttnKeys * kHeadDim * 2 + kAttnKeys * 4;  // offset of V in a block
+constexpr int kQ8BlockBytes = 2 * kQ8BlockV;
+
 // Two row tiles (A, B) of the same KV head that walk the same key segments: every K/V step feeds
 // 256 query rows.  Tile B may be empty (n_tok[1] == 0: the CTA runs tile A alone).  The same
 // kernel serves a decode plan's shared-prefix units with many query rows: its rows are then
@@ -125,8 +140,9 @@ struct PlanHeader {
   int32_t n_ctas;
   int32_t kv_type;       // RX_KV_BF16 or RX_KV_E4M3: the pool the plan's calls read
   int32_t max_refs;      // decode plans: the most partials of a request
-  int32_t pad32;
-  int64_t pad[12];
+  int32_t n_q8_tiles;    // extend plans for the 8-bit pool: Q8Tile table and expanded segments
+  int64_t off_q8_tiles, off_q8_stage;
+  int64_t pad[10];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
 
@@ -154,8 +170,13 @@ int launch_decode(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
 // The extend kernel on SM pairs over `n_items` items (one tile per CTA of a pair, kPairKeys-key
 // steps).
 int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
-                  const void* v_pool, const rx_kv_q8* kv, const void* q, void* o, float* lse,
-                  void* ws, void* stream);
+                  const void* v_pool, const void* q, void* o, float* lse, void* ws,
+                  void* stream);
+int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
+                     void* o, float* lse, void* ws, void* stream);
+// The expanded segments of an extend plan for the 8-bit pool (see Q8Tile), written to `stage`.
+int launch_expand_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const Q8Tile* tiles, int32_t n_tiles,
+                     void* stage, int32_t* status, void* stream);
 int launch_extend_pair(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                        const ExtSeg* segs, int32_t n_items, const void* k_pool,
                        const void* v_pool, const void* q, void* o, float* lse, int32_t* status,
@@ -165,15 +186,14 @@ int launch_extend_pair(const rx_kv_desc* d, const ExtItem* items, const ExtRow* 
 int make_pool_map(CUtensorMap* map, const void* pool, const rx_kv_desc* d);
 // The tensor-core attention kernel over `n_items` items of tables in device memory; with
 // part_o != nullptr every tile writes fp32 partial rows (normalised O, base-2 LSE) instead of o /
-// lse.  With `kv` the keys come from that 8-bit pool (k_pool and v_pool unused).
-// `status` is the plan's device status word.  With `cta_begin` (device, [n_ctas + 1]) the
+// lse.  `status` is the plan's device status word.  With `cta_begin` (device, [n_ctas + 1]) the
 // grid is n_ctas CTAs and CTA k runs items cta_begin[k] .. cta_begin[k + 1] - 1; with null the
 // items are dealt to one CTA per SM in snake order.
 int launch_attn_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
                       const ExtSeg* segs, int32_t n_items, const int32_t* cta_begin,
-                      int32_t n_ctas, const void* k_pool, const void* v_pool, const rx_kv_q8* kv,
-                      const void* q, void* o, float* lse, float* part_o, float* part_lse,
-                      int32_t* status, void* stream);
+                      int32_t n_ctas, const void* k_pool, const void* v_pool, const void* q,
+                      void* o, float* lse, float* part_o, float* part_lse, int32_t* status,
+                      void* stream);
 
 // The plan's second stream for a decode call on the current device (created on first use); all
 // NULL when the plan's calls launch a single kernel.

@@ -86,7 +86,7 @@ def test_pair_kernel_is_refused_for_the_8_bit_pool(librx):
     assert e.value.status == rx.RX_ERR_UNSUPPORTED
     plan.set_extend_kernel(rx.RX_EXTEND_TILES)
     rx.extend_plan(plan, _desc(), [0], [5], [3])
-    assert plan.rows() == 3 and plan.launches() == 1
+    assert plan.rows() == 3 and plan.launches() == 2
 
 
 def test_store_and_load_refusals(librx):
@@ -180,3 +180,23 @@ def test_decode_plan_checks_are_those_of_the_bf16_pool(librx):
         assert e.value.status == rx.RX_ERR_RANGE
     empty = _decode_plan(rx.RX_KV_E4M3, desc, np.zeros(0, np.int32))
     assert empty.launches() == 0 and empty.rows() == 0
+
+
+def test_extend_plan_for_the_8_bit_pool_reads_each_distinct_key_once(librx):
+    """A group's prefix is expanded once for all its members and tiles, a request's own keys once;
+    the workspace holds them: 64-key blocks of two 16 KiB images and two rows of scales."""
+    hkv, gp = 4, 300
+    desc = _desc(16, hkv, pool=1 << 20, rows=64, stride=4096)
+    new = [100, 1, 700, 0, 40]
+    prefix = [gp, gp + 64, gp, gp, 200]
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.extend_plan(plan, desc, [0, 1, 2, 3, 4], prefix, new, [0, 0, 0, 0, -1], [gp])
+    own = 100 + 65 + 700 + 240
+    assert plan.key_reads() == (gp + own) * hkv
+    tiles = sum(-(-n // 64) for n in (gp, 100, 65, 700, 240))
+    blocks = tiles * hkv * (2 * 64 * 256 + 2 * 64 * 4)
+    assert blocks <= plan.workspace_size() <= blocks + 65536
+    bf = rx.Plan()
+    rx.extend_plan(bf, desc, [0, 1, 2, 3, 4], prefix, new, [0, 0, 0, 0, -1], [gp])
+    assert bf.workspace_size() < 65536 and bf.launches() == 1
