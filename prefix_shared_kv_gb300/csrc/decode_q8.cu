@@ -5,25 +5,31 @@
 // The codes are exact in fp16, so both products run on the fp16 tensor cores with fp32 sums: a
 // query row is brought to fp16 by a power of two that puts its largest magnitude in [2^14, 2^15)
 // (what the conversion loses is below 2^-38 of that magnitude, and the power comes back in fp32).
-// The second product's weights are 2^(s_j + log2 vs_j - m'), m' the running maximum of
-// s_j + log2 vs_j: at most 1 whatever the scales are, so fp16 holds them to 2^-12 of their value
-// down to 2^-14 of the largest term, and V's scale costs no product of its own.  The softmax's sum
-// keeps its own running maximum of s_j.
+// The second product's weights are 2^(s_j - m') vs_j, m' a running reference for s_j + log2 vs_j:
+// at most 2^8 whatever the scales are, so fp16 holds them to 2^-11 of their value down to 2^-14,
+// and to 2^-25 below.  The softmax's sum has a reference m of its own.  Both only move (and O is only
+// rescaled) when some score of the warp's passes its reference by more than 2^8, which one vote per
+// step decides.
 //
-// Work items are the bf16 decode's: a chunk of one table row's keys for up to eight KV heads and
-// up to 16 stacked query rows (a shared prefix's members, or one request).  The queries are the
-// narrow side of the products: S^T = Kc Q^T (16 keys x 8 rows a tile) and O^T = Vc^T P^T, so one
-// request of a grouped-query model pads its rows to 8, not 16, and the codes, the wide operand,
-// are converted once for all the query rows.
-//   warps 0-7   one KV head each (where there are fewer than eight, the warps split a stage's keys
-//               and each leaves a partial result of its own): 32 keys a stage, online softmax and
-//               both products in registers.
-//   warps 8-11  gather the codes by slot with 16-byte cp.async (chunks XOR-swizzled by row) and
-//               the scales with 4-byte ones into a 3-stage ring that runs on across items; an
-//               entry outside the pool is flagged and read as zeros.
+// Work items are the bf16 decode's: a chunk of one table row's keys for a block of KV heads and
+// some stacked query rows (a shared prefix's members, or one request).  The queries are the narrow
+// side of the products: S^T = Kc Q^T (16 keys x 8 rows a tile) and O^T = Vc^T P^T, so one request
+// of a grouped-query model pads its rows to 8, not 16, and the codes, the wide operand, are
+// converted once for all the query rows of a warp.
+//   warps 0-7   one KV head each: 32 keys a stage, softmax and both products in registers.  Where a
+//               block has fewer heads than there are warps for it, the warps split the stage's keys
+//               and each leaves a partial result of its own.
+//   warps 8-11  gather the codes by slot with 16-byte cp.async (chunks XOR-swizzled by row) and the
+//               scales with 4-byte ones into a ring that runs on across items; an entry outside the
+//               pool is flagged and read as zeros.
+// Two forms.  Narrow items have up to 16 rows: eight heads a block, queries in registers, three
+// stages.  Wide ones have up to 64: a head's rows go to two warps (32 each), four heads a block;
+// the O tile alone takes 128 registers, so the queries lie in shared memory as fragments, a step
+// is 16 keys, and the producers hand registers to the consumers.
 // A persistent CTA per SM runs the list of items that the planner gave it.  Each item leaves
-// normalised fp32 partial rows and base-2 log-sum-exps, which a second kernel merges; it is
-// launched beside the first one (programmatic dependent launch) and waits there for its end.
+// normalised fp32 partial rows and base-2 log-sum-exps, which a last kernel merges.  The kernels are
+// chained by programmatic dependent launch: the narrow one starts as SMs come free of the wide
+// one, and the merge waits for both.
 // Waits are bounded; one that runs out records RX_ERR_TIMEOUT and every role leaves.
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -54,22 +60,37 @@ struct Params {
   int64_t pool_size;
   int32_t* status;
   const int32_t* cta_begin;  // per-CTA item lists: [gridDim.x + 1] starts
+  bool after_wide;           // the wide kernel was launched before this (narrow) one
 };
 
-constexpr int kWarps = 8;              // consumers
-constexpr int kProducers = 128;        // threads
+constexpr int kWarps = 8;        // consumers
+constexpr int kProducers = 128;  // threads
 constexpr int kThreads = 32 * kWarps + kProducers;
-constexpr int kWarpKeys = kQ8WarpKeys;  // keys a warp takes from a stage
-constexpr int kRows = kWarps * kWarpKeys;        // (key, head) rows of K and of V per stage
-constexpr int kHalf = kRows * kHeadDim;          // 32 KiB of codes
-constexpr int kOffScale = 2 * kHalf;             // K scales, then V scales, of the rows
-constexpr int kStageBytes = 2 * kHalf + 2 * kRows * 4;
-constexpr int kStages = 3;
-constexpr int kOffBar = kStages * kStageBytes;   // full[kStages], empty[kStages], abort
-constexpr int kSmem = kOffBar + 2 * kStages * 8 + 16;
-constexpr int kNoKey = INT32_MIN;      // past an item's keys
+// Registers: the launch's 168 a thread; the wide form moves them to its consumers.
+constexpr int kRegsLaunch = 168, kRegsConsumer = 216, kRegsProducer = 72;
+static_assert(2 * kRegsConsumer + kRegsProducer == 3 * kRegsLaunch, "register split");
+constexpr int kNoKey = INT32_MIN;  // past an item's keys
 constexpr uint64_t kWaitNs = 2000000000ull;
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+constexpr float kUnset = -1e30f;   // a reference no score has moved yet
+
+// HB = 1 << HBL KV heads a block.
+template <bool WIDE, int HBL>
+struct Form {
+  static constexpr int HB = 1 << HBL;
+  static constexpr int kRowWarps = WIDE ? 2 : 1;               // warps that share a head's rows
+  static constexpr int kRows = kWarps / kRowWarps * kQ8WarpKeys;  // (key, head) rows of a stage
+  static constexpr int NK = kRows / HB;                        // keys of a stage
+  static constexpr int kStages = WIDE ? 4 : 3;
+  static constexpr int kHalf = kRows * kHeadDim;               // codes of K, then of V
+  static constexpr int kOffScale = 2 * kHalf;                  // K scales, then V scales, [key][head]
+  static constexpr int kStageBytes = 2 * kHalf + 2 * kRows * 4;
+  static constexpr int kOffBar = kStages * kStageBytes;        // full[], empty[], abort
+  static constexpr int kOffQ = kOffBar + 2 * kStages * 8 + 64 - (2 * kStages * 8) % 64;
+  static constexpr int kQWarp = 8 * 4 * 32 * 8;                // a warp's query fragments (wide)
+  static constexpr int kSmem = kOffQ + (WIDE ? kWarps * kQWarp : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(NK % 32 == 0, "a stage holds whole groups of 32 keys");
+};
 
 __device__ __forceinline__ uint32_t row_off(int r, int c) {  // 16-byte chunk c of 128-byte row r
   return (uint32_t)(r * kHeadDim + ((c ^ (r & 7)) << 4));
@@ -89,9 +110,10 @@ __device__ __forceinline__ void arrive_on_copies(uint32_t mbar) {
 // instruction copies four rows (512 contiguous bytes where a block has four heads or more), and the
 // warps take every fourth instruction.  A lane holds the table entries of keys lane, lane + 32, ...
 // of the stage, fetched a stage ahead and checked once; the copies take them by shuffle.
-template <int HBL>
+template <bool WIDE, int HBL>
 __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
-  constexpr int HB = 1 << HBL, NK = kRows / HB, S = NK / 32;
+  using F = Form<WIDE, HBL>;
+  constexpr int HB = F::HB, NK = F::NK, S = NK / 32;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kWarps;
   const int c = lane & 7, sub = lane >> 3;
   uint32_t g = 0;  // stages filled so far
@@ -112,8 +134,8 @@ __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
     };
     fetch(0);
     for (int k0 = 0; k0 < nkeys; k0 += NK, ++g) {
-      const int st = g % kStages;
-      const uint32_t full = base + kOffBar + 8 * st, empty = full + 8 * kStages;
+      const int st = g % F::kStages;
+      const uint32_t full = base + F::kOffBar + 8 * st, empty = full + 8 * F::kStages;
       int sl[S];
 #pragma unroll
       for (int i = 0; i < S; ++i) {
@@ -124,27 +146,27 @@ __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
         }
       }
       if (k0 + NK < nkeys) fetch(k0 + NK);
-      const bool ok = g < kStages ||
-                      tc::mbar_wait(empty, (g / kStages - 1) & 1, abort, p.status, kWaitNs);
+      const bool ok = g < F::kStages ||
+                      tc::mbar_wait(empty, (g / F::kStages - 1) & 1, abort, p.status, kWaitNs);
       if (__any_sync(0xffffffffu, !ok)) {
         cp_async_wait<0>();
         return;
       }
-      const uint32_t kb = base + st * kStageBytes, vb = kb + kHalf, sb = kb + kOffScale;
+      const uint32_t kb = base + st * F::kStageBytes, vb = kb + F::kHalf, sb = kb + F::kOffScale;
 #pragma unroll
-      for (int i = 0; i < kRows / 16; ++i) {
+      for (int i = 0; i < F::kRows / 16; ++i) {
         const int f = 16 * i + 4 * w + sub;
         const int key = f >> HBL, h = f & (HB - 1);
         // (16 i .. 16 i + 15 lie in one run of 32 keys: the register is known here)
         const int slot = __shfl_sync(0xffffffffu, sl[(16 * i) >> (HBL + 5)], key & 31);
         const int64_t off =
             slot >= 0 ? ((int64_t)slot * p.hkv + head0 + h) * kHeadDim + 16 * c : 0;
-        const uint32_t so = row_off(((key >> 5) * HB + h) * kWarpKeys + (key & 31), c);
+        const uint32_t so = row_off(((key >> 5) * HB + h) * kQ8WarpKeys + (key & 31), c);
         cp_async16(kb + so, p.k_code + off, slot >= 0);
         cp_async16(vb + so, p.v_code + off, slot >= 0);
       }
 #pragma unroll
-      for (int i = 0; i < kRows / 128; ++i) {  // scales, [key][head]
+      for (int i = 0; i < F::kRows / 128; ++i) {  // scales, [key][head]
         const int f = 128 * i + 32 * w + lane;
         const int key = f >> HBL, h = f & (HB - 1);
         int slot = 0;
@@ -155,7 +177,7 @@ __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
         }
         const int64_t off = slot >= 0 ? (int64_t)slot * p.hkv + head0 + h : 0;
         cp_async4(sb + 4 * f, p.k_scale + off, slot >= 0);
-        cp_async4(sb + 4 * (kRows + f), p.v_scale + off, slot >= 0);
+        cp_async4(sb + 4 * (F::kRows + f), p.v_scale + off, slot >= 0);
       }
       arrive_on_copies(full);
     }
@@ -170,24 +192,29 @@ __device__ __forceinline__ float lg2(float x) {
 }
 
 // One item on a consumer warp: NT tiles of 8 query rows.  Returns false when a wait gave up.
-template <int NT, int HBL>
-__device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, const uint8_t* smem,
-                         uint32_t& gs, volatile int* abort) {
+template <int NT, bool WIDE, int HBL>
+__device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uint32_t base,
+                                         uint8_t* smem, uint32_t& gs, volatile int* abort) {
+  using F = Form<WIDE, HBL>;
+  constexpr int HB = F::HB, NK = F::NK;
+  constexpr int KT = WIDE ? 1 : 2;  // 16-key tiles of a step
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  constexpr int HB = 1 << HBL, nk = kRows / HB;
-  const int head = it.head_block * HB + (warp & (HB - 1));
-  const int split = warp >> HBL;
+  const int kw = warp % (kWarps / F::kRowWarps);  // the warp's 32-key run of a stage
+  const int row0 = warp / (kWarps / F::kRowWarps) * (8 * NT);
+  const int head = it.head_block * HB + (kw & (HB - 1));
+  const int split = kw >> HBL;
   const int nkeys = it.k_end - it.k_begin;
   const int rows = it.n_tok * p.gq;
 
   // Query fragments: position 2c + e of a 16-wide step holds d = 16 step + 4c + e, and 8 + 2c + e
   // holds 16 step + 4c + 2 + e, as the conversion of four neighbouring codes leaves K.
-  uint32_t qf[8][NT][2];
+  uint2 qf[WIDE ? 1 : 8][WIDE ? 1 : NT];
+  uint2* sq = reinterpret_cast<uint2*>(smem + F::kOffQ + warp * F::kQWarp) + lane;
   float qs[NT][2];  // scale_log2 and the row's power of two, for the columns 2c and 2c + 1
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = 8 * n + g;
+    const int r = row0 + 8 * n + g;
     uint2 x[8];
     uint32_t m = 0;
     if (r < rows) {
@@ -211,10 +238,14 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
     const float down = __uint_as_float((uint32_t)(e - 14) << 23);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      qf[k][n][0] = pack_f16(__uint_as_float(x[k].x << 16) * up,
-                             __uint_as_float(x[k].x & 0xffff0000u) * up);
-      qf[k][n][1] = pack_f16(__uint_as_float(x[k].y << 16) * up,
-                             __uint_as_float(x[k].y & 0xffff0000u) * up);
+      const uint2 y = make_uint2(pack_f16(__uint_as_float(x[k].x << 16) * up,
+                                          __uint_as_float(x[k].x & 0xffff0000u) * up),
+                                 pack_f16(__uint_as_float(x[k].y << 16) * up,
+                                          __uint_as_float(x[k].y & 0xffff0000u) * up));
+      if constexpr (WIDE)
+        sq[(k * NT + n) * 32] = y;  // read by this lane only
+      else
+        qf[k][n] = y;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -222,114 +253,133 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
   }
 
   float o[8][NT][4];
-  float m1[NT][2], m2[NT][2], l[NT][2];
+  // references of the sum and of the weights, 2^(m1 - m2), the sum (this lane's keys)
+  float m1[NT][2], m2[NT][2], cw[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      m1[n][j] = m2[n][j] = -CUDART_INF_F;
-      l[n][j] = 0.f;
+      m1[n][j] = m2[n][j] = kUnset;
+      cw[n][j] = l[n][j] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
   }
 
-  for (int k0 = 0; k0 < nkeys; k0 += nk, ++gs) {
-    const int st = gs % kStages;
-    const uint32_t full = base + kOffBar + 8 * st;
-    const bool ok = tc::mbar_wait(full, (gs / kStages) & 1, abort, p.status, kWaitNs);
+  for (int k0 = 0; k0 < nkeys; k0 += NK, ++gs) {
+    const int st = gs % F::kStages;
+    const uint32_t full = base + F::kOffBar + 8 * st;
+    const bool ok = tc::mbar_wait(full, (gs / F::kStages) & 1, abort, p.status, kWaitNs);
     if (__any_sync(0xffffffffu, !ok)) return false;
-    const int left = nkeys - k0 - split * kWarpKeys;  // keys of this warp in the stage
-    if (left > 0) {
-      const uint32_t kb = base + st * kStageBytes + warp * kWarpKeys * kHeadDim;
-      const uint32_t vb = kb + kHalf;
-      const float* sc = reinterpret_cast<const float*>(smem + st * kStageBytes + kOffScale) +
-                        split * kWarpKeys * HB + (warp & (HB - 1));
-      float s[2][NT][4];
+    const int left = nkeys - k0 - split * kQ8WarpKeys;  // keys of this warp in the stage
+    const uint32_t kb = base + st * F::kStageBytes + kw * kQ8WarpKeys * kHeadDim;
+    const uint32_t vb = kb + F::kHalf;
+    const float* sc = reinterpret_cast<const float*>(smem + st * F::kStageBytes + F::kOffScale) +
+                      split * kQ8WarpKeys * HB + (kw & (HB - 1));
+#pragma unroll 1
+    for (int t0 = 0; t0 < 2; t0 += KT) {
+      if (16 * t0 >= left) break;
+      float s[KT][NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
 #pragma unroll
       for (int k2 = 0; k2 < 4; ++k2)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < KT; ++t) {
           uint32_t x[4];
-          const int r = 16 * t + (lane & 15);
+          const int r = 16 * (t0 + t) + (lane & 15);
           ldsm_x4(kb + row_off(r, 2 * k2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t a[4] = {e4m3x2_to_f16x2(x[2 * h]), e4m3x2_to_f16x2(x[2 * h + 1]),
                                    e4m3x2_hi_to_f16x2(x[2 * h]), e4m3x2_hi_to_f16x2(x[2 * h + 1])};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_16816_f16(s[t][n], a, qf[2 * k2 + h][n][0], qf[2 * k2 + h][n][1]);
+            for (int n = 0; n < NT; ++n) {
+              uint2 y;
+              if constexpr (WIDE)
+                y = sq[((2 * k2 + h) * NT + n) * 32];
+              else
+                y = qf[2 * k2 + h][n];
+              mma_16816_f16(s[t][n], a, y.x, y.y);
+            }
           }
         }
-      // scales, masks, the two running maxima (columns 2c + j; keys 16 t + 8 h + g)
-      float lv[2][2];
+      // scales and masks (columns 2c + j; keys 16 t + 8 h + g); how far the scores pass the
+      // references
+      float vs[KT][2], lv[KT][2], over = kUnset;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = 16 * t + 8 * h + g;
+          const int key = 16 * (t0 + t) + 8 * h + g;
           const float ks = sc[key * HB];
-          lv[t][h] = lg2(sc[kRows + key * HB]);
+          vs[t][h] = sc[F::kRows + key * HB];
+          lv[t][h] = lg2(vs[t][h]);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              s[t][n][2 * h + j] =
-                  key < left ? s[t][n][2 * h + j] * ks * qs[n][j] : -CUDART_INF_F;
-        }
-      uint32_t pt[2][NT][2];  // P^T: columns are query rows, two keys a register
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float a2[2], p2[2][2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x1 = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]), fmaxf(s[1][n][j], s[1][n][2 + j]));
-          float x2 = fmaxf(fmaxf(s[0][n][j] + lv[0][0], s[0][n][2 + j] + lv[0][1]),
-                           fmaxf(s[1][n][j] + lv[1][0], s[1][n][2 + j] + lv[1][1]));
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) {
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-            x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, off));
-          }
-          x1 = fmaxf(x1, m1[n][j]);
-          x2 = fmaxf(x2, m2[n][j]);
-          // no finite score yet: any finite reference serves
-          const float r1 = x1 == -CUDART_INF_F ? 0.f : x1, r2 = x2 == -CUDART_INF_F ? 0.f : x2;
-          const float a1 = fast_exp2(m1[n][j] - r1);
-          a2[j] = fast_exp2(m2[n][j] - r2);
-          m1[n][j] = x1;
-          m2[n][j] = x2;
-          float sum = 0.f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float v = s[t][n][2 * h + j];
-              sum += fast_exp2(v - r1);
-              p2[t][h][j] = fast_exp2(v + lv[t][h] - r2);
+            for (int j = 0; j < 2; ++j) {
+              const float v = key < left ? s[t][n][2 * h + j] * ks * qs[n][j] : -CUDART_INF_F;
+              s[t][n][2 * h + j] = v;
+              over = fmax3(over, v - m1[n][j], v + lv[t][h] - m2[n][j]);
             }
-          l[n][j] = l[n][j] * a1 + sum;
         }
+      if (__any_sync(0xffffffffu, over > 8.f)) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) pt[t][n][h] = movm_t(pack_f16(p2[t][h][0], p2[t][h][1]));
+          for (int j = 0; j < 2; ++j) {
+            float x1 = m1[n][j], x2 = m2[n][j];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][n][e] *= a2[e & 1];
+              for (int h = 0; h < 2; ++h) {
+                x1 = fmaxf(x1, s[t][n][2 * h + j]);
+                x2 = fmaxf(x2, s[t][n][2 * h + j] + lv[t][h]);
+              }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+              x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, off));
+            }
+            l[n][j] *= fast_exp2(m1[n][j] - x1);
+            const float a2 = fast_exp2(m2[n][j] - x2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[i][n][j] *= a2;
+              o[i][n][2 + j] *= a2;
+            }
+            m1[n][j] = x1;
+            m2[n][j] = x2;
+            // (no key with a V scale yet: nothing to weigh; above 2^126 the weights themselves
+            // are below the smallest float)
+            cw[n][j] = x2 == kUnset ? 0.f : fast_exp2(fminf(x1 - x2, 126.f));
+          }
       }
+      uint32_t pt[KT][NT][2];  // P^T: columns are query rows, two keys a register
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float e = fast_exp2(s[t][n][2 * h + j] - m1[n][j]);
+              l[n][j] += e;
+              w[j] = e * vs[t][h] * cw[n][j];
+            }
+            pt[t][n][h] = movm_t(pack_f16(w[0], w[1]));
+          }
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int i2 = 0; i2 < 4; ++i2) {
           uint32_t x[4];
-          const int r = 16 * t + (lane & 15);
+          const int r = 16 * (t0 + t) + (lane & 15);
           ldsm_x4_t(vb + row_off(r, 2 * i2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -345,11 +395,11 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
         }
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(full + 8 * kStages);
+    if (lane == 0) tc::mbar_arrive(full + 8 * F::kStages);
   }
 
   // partial rows: split, KV head, row.  A split without keys has none (the merge knows).
-  if (split * kWarpKeys >= nkeys) return true;
+  if (split * kQ8WarpKeys >= nkeys) return true;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -357,50 +407,58 @@ __device__ bool run_item(const Params& p, const DecItem& it, uint32_t base, cons
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
         l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
-      const int r = 8 * n + 2 * c + j;
+      const int r = row0 + 8 * n + 2 * c + j;
       if (r >= rows) continue;
       const bool none = l[n][j] == 0.f;
-      // (m1 = -inf with a sum: NaN scores only, and the sum says so)
-      const float r1 = m1[n][j] == -CUDART_INF_F ? 0.f : m1[n][j];
-      const float f = none ? 0.f : fast_exp2(m2[n][j] - r1) / l[n][j];
+      const float f = none ? 0.f : fast_exp2(m2[n][j] - m1[n][j]) / l[n][j];
       const int64_t row = (int64_t)it.part + ((int64_t)split * p.hkv + head) * rows + r;
       float* dst = p.part_o + row * kHeadDim + 2 * g;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[i][n][j] * f, o[i][n][2 + j] * f);
-      if (g == 0) p.part_lse[row] = none ? -CUDART_INF_F : r1 + __log2f(l[n][j]);
+      if (g == 0) p.part_lse[row] = none ? -CUDART_INF_F : m1[n][j] + __log2f(l[n][j]);
     }
   }
   return true;
 }
 
-template <int HBL>
+template <bool WIDE, int HBL>
 __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) {
+  using F = Form<WIDE, HBL>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + kOffBar + 2 * kStages * 8);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + F::kOffBar + 2 * F::kStages * 8);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(base + kOffBar + 8 * i, kProducers);
-      tc::mbar_init(base + kOffBar + 8 * (kStages + i), kWarps);
+    for (int i = 0; i < F::kStages; ++i) {
+      tc::mbar_init(base + F::kOffBar + 8 * i, kProducers);
+      tc::mbar_init(base + F::kOffBar + 8 * (F::kStages + i), kWarps);
     }
     *abort = 0;
   }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x >= 32 * kWarps) {
-    producer<HBL>(p, base, abort);
-    return;
+    if constexpr (WIDE) tc::regs_dec<kRegsProducer>();
+    producer<WIDE, HBL>(p, base, abort);
+  } else {
+    if constexpr (WIDE) tc::regs_inc<kRegsConsumer>();
+    uint32_t gs = 0;
+    for (int k = 0;; ++k) {
+      const int idx = item_at(p, k);
+      if (idx < 0) break;
+      const DecItem it = p.items[idx];
+      bool ok;
+      if constexpr (WIDE)
+        ok = run_item<4, WIDE, HBL>(p, it, base, smem, gs, abort);
+      else
+        ok = it.kind == 0 ? run_item<1, WIDE, HBL>(p, it, base, smem, gs, abort)
+                          : run_item<2, WIDE, HBL>(p, it, base, smem, gs, abort);
+      if (!ok) break;
+    }
   }
-  uint32_t gs = 0;
-  for (int k = 0;; ++k) {
-    const int idx = item_at(p, k);
-    if (idx < 0) return;
-    const DecItem it = p.items[idx];
-    const bool ok = it.kind == 0 ? run_item<1, HBL>(p, it, base, smem, gs, abort)
-                                 : run_item<2, HBL>(p, it, base, smem, gs, abort);
-    if (!ok) return;
-  }
+  // the merge behind this kernel waits for this one only
+  if constexpr (!WIDE)
+    if (p.after_wide) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // W warps per (request, query head), W from the longest list of partials: warp w takes partials
@@ -523,22 +581,38 @@ cudaError_t launch_merge(const Params& p, const uint8_t* base, const PlanHeader*
                             (int)h->batch, p.hq, p.gq, static_cast<__nv_bfloat16*>(o), lse);
 }
 
-template <int HBL>
+template <bool WIDE, int HBL>
 cudaError_t launch_partials(const Params& p, int grid, cudaStream_t stream) {
   // kernel attributes belong to the current device: set once per device (bit d of the mask)
   static std::atomic<uint64_t> attr_set{0};
+  constexpr int kSmem = Form<WIDE, HBL>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!((attr_set.load() >> dev) & 1)) {
-    e = cudaFuncSetAttribute(decode_q8_kernel<HBL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem);
+    // the wide form's register split balances only if every thread starts with kRegsLaunch (with
+    // fewer the consumers would wait for registers that never come): any other build is refused
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, decode_q8_kernel<WIDE, HBL>);
+    if (e != cudaSuccess) return e;
+    if (WIDE && fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(decode_q8_kernel<WIDE, HBL>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(1ull << dev);
   }
-  decode_q8_kernel<HBL><<<grid, kThreads, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute beside = {};
+  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  beside.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &beside;
+  cfg.numAttrs = p.after_wide ? 1 : 0;  // what comes before a call's first kernel is not ours
+  return cudaLaunchKernelEx(&cfg, decode_q8_kernel<WIDE, HBL>, p);
 }
 
 }  // namespace
@@ -558,32 +632,40 @@ int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   p.hkv = d->num_kv_heads;
   p.gq = d->num_q_heads / d->num_kv_heads;
   p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  p.items = reinterpret_cast<const DecItem*>(base + h->off_items);
   p.rows = reinterpret_cast<const int32_t*>(base + h->off_rows);
   p.part_o = reinterpret_cast<float*>(base + h->off_part_o);
   p.part_lse = reinterpret_cast<float*>(base + h->off_part_lse);
   p.pool_size = d->pool_size;
   p.status = reinterpret_cast<int32_t*>(base + offsetof(PlanHeader, status));
-  p.cta_begin = reinterpret_cast<const int32_t*>(base + h->off_cta);
   cudaStream_t s = (cudaStream_t)stream;
+  const int hbl = q8_head_block_log2(p.hkv);
+  cudaError_t e = cudaSuccess;
+  if (h->n_wide > 0) {
+    p.items = reinterpret_cast<const DecItem*>(base + h->off_wide);
+    p.cta_begin = reinterpret_cast<const int32_t*>(base + h->off_wide_cta);
+    p.after_wide = false;
+    e = hbl == 3   ? launch_partials<true, 2>(p, h->n_wide_ctas, s)
+        : hbl == 2 ? launch_partials<true, 1>(p, h->n_wide_ctas, s)
+                   : launch_partials<true, 0>(p, h->n_wide_ctas, s);
+    if (e != cudaSuccess) return (int)e;
+  }
   if (h->n_items > 0) {
-    cudaError_t e = cudaSuccess;
-    switch (q8_head_block_log2(d->num_kv_heads)) {
-      case 3: e = launch_partials<3>(p, h->n_ctas, s); break;
-      case 2: e = launch_partials<2>(p, h->n_ctas, s); break;
-      case 1: e = launch_partials<1>(p, h->n_ctas, s); break;
-      default: e = launch_partials<0>(p, h->n_ctas, s); break;
-    }
+    p.items = reinterpret_cast<const DecItem*>(base + h->off_items);
+    p.cta_begin = reinterpret_cast<const int32_t*>(base + h->off_cta);
+    p.after_wide = h->n_wide > 0;
+    e = hbl == 3   ? launch_partials<false, 3>(p, h->n_ctas, s)
+        : hbl == 2 ? launch_partials<false, 2>(p, h->n_ctas, s)
+        : hbl == 1 ? launch_partials<false, 1>(p, h->n_ctas, s)
+                   : launch_partials<false, 0>(p, h->n_ctas, s);
     if (e != cudaSuccess) return (int)e;
   }
   if (h->batch > 0) {
-    // (one partial a request and head: a single read; 8 or more: eight reads in flight per warp)
-    const cudaError_t e = h->max_refs <= 8    ? launch_merge<1>(p, base, h, o, lse, s)
-                          : h->max_refs <= 32 ? launch_merge<2>(p, base, h, o, lse, s)
-                                              : launch_merge<8>(p, base, h, o, lse, s);
-    if (e != cudaSuccess) return (int)e;
+    // one warp a row up to 8 partials (all its reads in flight at once), two up to 32, else eight
+    e = h->max_refs <= 8    ? launch_merge<1>(p, base, h, o, lse, s)
+        : h->max_refs <= 32 ? launch_merge<2>(p, base, h, o, lse, s)
+                            : launch_merge<8>(p, base, h, o, lse, s);
   }
-  return (int)cudaGetLastError();
+  return (int)e;
 }
 
 }  // namespace rx

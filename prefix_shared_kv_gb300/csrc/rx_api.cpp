@@ -373,7 +373,7 @@ rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches) {
   // kernel for the others, and the merge whenever there are requests
   // (an extend over an 8-bit pool expands the plan's keys in a kernel of its own first)
   *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3))
-                              : (h.n_xitems > 0) + (h.n_items > 0) + (h.batch > 0);
+                              : (h.n_xitems > 0) + (h.n_wide > 0) + (h.n_items > 0) + (h.batch > 0);
   return RX_OK;
 }
 
@@ -505,41 +505,105 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   std::vector<int32_t> rows;
   std::vector<std::vector<DecMergeRef>> refs(batch);
   int64_t npart = 0;
-  // 8-bit pools have kinds, head blocks and splits of their own (see kQ8WarpKeys)
+  // 8-bit pools have kinds, head blocks and splits of their own (see kQ8WarpKeys): kind 2 is wide
   const bool q8 = plan->kv_next == RX_KV_E4M3;
-  const int q8_hb = 1 << q8_head_block_log2(hkv), splits = q8 ? 8 / q8_hb : 1;
-  const int max_tok = (q8 ? kQ8MaxRows : 64) / gq;
-  auto kind_of_rows = [&](int r) { return q8 ? r > 8 : r <= 16 ? 0 : (r <= 32 ? 1 : 2); };
-  auto hb_of = [&](int kind) { return q8 ? q8_hb : kind == 0 ? 8 : (kind == 1 ? 4 : 2); };
+  const int q8_hb = 1 << q8_head_block_log2(hkv), q8_whb = std::max(1, q8_hb / 2);
+  const int max_tok = (q8 ? kQ8MaxWideRows : 64) / gq;
+  auto kind_of_rows = [&](int r) {
+    return q8 ? (r > kQ8MaxRows ? 2 : r > 8) : r <= 16 ? 0 : (r <= 32 ? 1 : 2);
+  };
+  auto hb_of = [&](int kind) {
+    return q8 ? (kind == 2 ? q8_whb : q8_hb) : kind == 0 ? 8 : (kind == 1 ? 4 : 2);
+  };
+  auto splits_of = [&](int kind) { return !q8 ? 1 : (kind == 2 ? 4 : 8) / hb_of(kind); };
+  auto stage_keys = [&](int kind) {  // keys of a pipeline stage
+    return q8 ? splits_of(kind) * kQ8WarpKeys : kDecRows / hb_of(kind);
+  };
 
+  // The units' keys: a shared prefix for a tile of its members, then each request's own.
+  struct Span {
+    int kind, n_rows, len;
+  };
+  std::vector<Span> spans;  // 8-bit pool: for the choice of the items' length
   // bytes of K+V per key for one KV head
-  const double key_bytes = q8 ? 2.0 * (kHeadDim + 4) : 2.0 * kHeadDim * 2;
+  const double key_bytes = 2.0 * kHeadDim * 2;
   double total = 0;
   for (int g = 0; g < num_groups; ++g)
-    if (!members[g].empty() && group_prefix_len[g] > node_lo(g))
-      total += (double)(group_prefix_len[g] - node_lo(g)) * hkv * key_bytes *
-               ((members[g].size() + max_tok - 1) / max_tok);
-  for (int b = 0; b < batch; ++b)
-    total += (double)(seq_len[b] - (grp[b] >= 0 ? group_prefix_len[grp[b]] : 0)) * hkv * key_bytes;
+    if (!members[g].empty() && group_prefix_len[g] > node_lo(g)) {
+      const int len = group_prefix_len[g] - node_lo(g);
+      total += (double)len * hkv * key_bytes * ((members[g].size() + max_tok - 1) / max_tok);
+      for (size_t t0 = 0; q8 && t0 < members[g].size(); t0 += max_tok) {
+        const int r = (int)std::min<size_t>(max_tok, members[g].size() - t0) * gq;
+        spans.push_back({kind_of_rows(r), r, len});
+      }
+    }
+  for (int b = 0; b < batch; ++b) {
+    const int len = seq_len[b] - (grp[b] >= 0 ? group_prefix_len[grp[b]] : 0);
+    total += (double)len * hkv * key_bytes;
+    if (q8 && len > 0) spans.push_back({0, gq, len});
+  }
   // bytes of K/V per mma.sync item: about three items per SM, but no item under 1 MiB (smaller
   // ones spend more on their own start and partial write-out than on the read)
   const int sms = device_sms();
   const double target = std::min(4.0 * 1048576, std::max(1048576.0, total / (3.0 * sms)));
 
-  // Keys per item over an 8-bit pool, in whole stages: enough items for four per SM, so that their
-  // lists come out even, but none under kQ8MinStages while there is one for every SM.
-  const int q8_nk = splits * kQ8WarpKeys;
-  int q8_chunk = q8_nk;
-  if (q8) {
-    const double stages = total / (q8_nk * q8_hb * key_bytes);
-    const double per = std::max(stages / (4.0 * sms), std::min<double>(kQ8MinStages, stages / sms));
-    q8_chunk = q8_nk * (int)std::min(4096.0, std::max(1.0, std::ceil(per)));
+  // 8-bit pool: stages per item, for the narrow and the wide items.  An item costs, beyond its
+  // stages, its start and its partial rows (written, and read by the merge), in stages of copy time.
+  // Shorter items even the lists out (and fill the GPU when there is little work), longer ones pay
+  // less per item: of a few lengths the one with the shortest longest list is taken, the longest of
+  // equals.
+  int q8_stages[2] = {1, 1};
+  auto item_cost = [&](int kind, int n_rows, int stages) {  // in hundredths of a stage
+    const int hb = hb_of(kind), rows_stage = kind == 2 ? 128 : 256;
+    return 100ll * stages + 150 + 100ll * 2 * n_rows * hb * kHeadDim * 4 / (rows_stage * 264);
+  };
+  for (int wide = 0; q8 && wide < 2; ++wide) {
+    int64_t stages = 0;
+    auto of = [&](const Span& u) { return (u.kind == 2) == (wide == 1); };
+    for (const Span& u : spans)
+      if (of(u))
+        stages += (int64_t)((u.len + stage_keys(u.kind) - 1) / stage_keys(u.kind)) *
+                  (hkv / hb_of(u.kind));
+    int64_t best = INT64_MAX;
+    for (int per : {1, 2, 3, 4, 6, 8, 12}) {  // items per SM
+      const int64_t n = std::max<int64_t>(1, (stages + (int64_t)per * sms - 1) / ((int64_t)per * sms));
+      if (per > 1 && n < 2) break;
+      std::vector<int64_t> costs;
+      int64_t sum = 0;
+      for (const Span& u : spans) {
+        if (!of(u)) continue;
+        const int64_t st = (u.len + stage_keys(u.kind) - 1) / stage_keys(u.kind);
+        const int64_t parts = (st + n - 1) / n;
+        for (int64_t i = 0; i < parts; ++i) {
+          const int64_t c = item_cost(u.kind, u.n_rows, (int)((st + parts - 1) / parts));
+          for (int h = 0; h < hkv / hb_of(u.kind); ++h) costs.push_back(c);
+          sum += c * (hkv / hb_of(u.kind));
+        }
+      }
+      std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
+      int64_t longest = sum / sms;
+      if (costs.size() <= (size_t)16 * sms) {
+        std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+        for (int k = 0; k < sms; ++k) ends.push(0);
+        for (int64_t c : costs) {
+          const int64_t e = ends.top() + c;
+          ends.pop();
+          ends.push(e);
+          longest = std::max(longest, e);
+        }
+      }
+      if (longest < best) {
+        best = longest;
+        q8_stages[wide] = (int)std::min<int64_t>(n, 1 << 16);
+      }
+    }
   }
   auto chunks = [&](int len, int kind, std::vector<std::pair<int, int>>& out) {
     const int hb = std::min(hb_of(kind), hkv);
-    const int nk = q8 ? splits * kQ8WarpKeys : kDecRows / hb_of(kind);
+    const int nk = stage_keys(kind);
     int max_keys = (int)(target / (hb * key_bytes));
-    max_keys = q8 ? q8_chunk : std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
+    max_keys = q8 ? q8_stages[kind == 2] * nk
+                  : std::max(64, std::min(kDecMaxKeysPerItem, max_keys));
     const int n = (len + max_keys - 1) / max_keys;
     int c = (len + n - 1) / n;
     c = (c + nk - 1) / nk * nk;
@@ -549,8 +613,8 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   };
   std::vector<std::pair<int, int>> ch;
   // The references of one request to a unit of `len` keys: one partial per split that has keys.
-  auto refer = [&](int b, int64_t part, int len, int n_rows, int row) {
-    for (int k = 0; k < splits && k * kQ8WarpKeys < len; ++k)
+  auto refer = [&](int b, int kind, int64_t part, int len, int n_rows, int row) {
+    for (int k = 0; k < splits_of(kind) && k * kQ8WarpKeys < len; ++k)
       refs[b].push_back({(int32_t)(part + (int64_t)k * hkv * n_rows), n_rows, row, 0});
   };
 
@@ -621,11 +685,11 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
       chunks(hi - lo, kind, ch);
       for (auto& c : ch) {
         const int64_t part = npart;
-        npart += (int64_t)splits * hkv * n_tok * gq;
+        npart += (int64_t)splits_of(kind) * hkv * n_tok * gq;
         units.push_back(
             {kind, req_idx[mem[t0]], lo + c.first, lo + c.second, row_begin, n_tok, part});
         for (int i = 0; i < n_tok; ++i)
-          refer(mem[t0 + i], part, c.second - c.first, n_tok * gq, i * gq);
+          refer(mem[t0 + i], kind, part, c.second - c.first, n_tok * gq, i * gq);
       }
     }
   }
@@ -637,50 +701,58 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     chunks(seq_len[b] - k0, 0, ch);
     for (auto& c : ch) {
       const int64_t part = npart;
-      npart += (int64_t)splits * hkv * gq;
+      npart += (int64_t)splits_of(0) * hkv * gq;
       units.push_back({0, req_idx[b], k0 + c.first, k0 + c.second, row_begin, 1, part});
-      refer(b, part, c.second - c.first, gq, 0);
+      refer(b, 0, part, c.second - c.first, gq, 0);
     }
   }
   if (npart > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
 
-  std::vector<DecItem> items;
+  std::vector<DecItem> items, wide;
   for (const Unit& u : units) {
     const int hb = hb_of(u.kind);
     for (int h = 0; h * hb < hkv; ++h)
-      items.push_back({u.kind, h, u.kv_row, u.k_begin, u.k_end, u.row_begin, u.n_tok,
-                       (int32_t)u.part});
+      (q8 && u.kind == 2 ? wide : items)
+          .push_back({u.kind, h, u.kv_row, u.k_begin, u.k_end, u.row_begin, u.n_tok,
+                      (int32_t)u.part});
     key_reads += (int64_t)(u.k_end - u.k_begin) * hkv;
   }
   auto cost = [&](const DecItem& it) {
-    return (double)(it.k_end - it.k_begin) * std::min(hb_of(it.kind), hkv);
+    return q8 ? (double)item_cost(it.kind, it.n_tok * gq,
+                                  (it.k_end - it.k_begin + stage_keys(it.kind) - 1) /
+                                      stage_keys(it.kind))
+              : (double)(it.k_end - it.k_begin) * std::min(hb_of(it.kind), hkv);
   };
-  std::stable_sort(items.begin(), items.end(),
-                   [&](const DecItem& a, const DecItem& b) { return cost(a) > cost(b); });
+  auto by_cost = [&](const DecItem& a, const DecItem& b) { return cost(a) > cost(b); };
+  std::stable_sort(items.begin(), items.end(), by_cost);
+  std::stable_sort(wide.begin(), wide.end(), by_cost);
 
-  // 8-bit pool: one list per CTA, each item (costliest first) to the list that is shortest so far
-  std::vector<int32_t> cta_begin;
-  if (q8 && !items.empty()) {
-    const int32_t G = (int32_t)std::min<int64_t>(sms, (int64_t)items.size());
-    using Slot = std::pair<int64_t, int32_t>;  // (length of the list, CTA)
+  // 8-bit pool: one list per CTA, each item (costliest first) to the list that is shortest so
+  // far; the table is stored list by list
+  auto deal = [&](std::vector<DecItem>& all, std::vector<int32_t>& begin) {
+    if (all.empty()) return;
+    const int32_t G = (int32_t)std::min<int64_t>(sms, (int64_t)all.size());
+    using Slot = std::pair<double, int32_t>;  // (length of the list, CTA)
     std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>> free_at;
-    for (int32_t k = 0; k < G; ++k) free_at.push({0, k});
-    std::vector<std::vector<int32_t>> lists(G);
-    for (size_t i = 0; i < items.size(); ++i) {
+    for (int32_t k = 0; k < G; ++k) free_at.push({0., k});
+    std::vector<std::vector<DecItem>> lists(G);
+    for (const DecItem& it : all) {
       const Slot s = free_at.top();
       free_at.pop();
-      lists[s.second].push_back((int32_t)i);
-      const int64_t st = (items[i].k_end - items[i].k_begin + q8_nk - 1) / q8_nk;
-      free_at.push({s.first + st * kQ8StageCost + kQ8ItemCost, s.second});
+      lists[s.second].push_back(it);
+      free_at.push({s.first + cost(it), s.second});
     }
-    std::vector<DecItem> by_cta;
-    by_cta.reserve(items.size());
-    cta_begin.push_back(0);
+    all.clear();
+    begin.push_back(0);
     for (const auto& l : lists) {
-      for (int32_t i : l) by_cta.push_back(items[i]);
-      cta_begin.push_back((int32_t)by_cta.size());
+      all.insert(all.end(), l.begin(), l.end());
+      begin.push_back((int32_t)all.size());
     }
-    items.swap(by_cta);
+  };
+  std::vector<int32_t> cta_begin, wide_begin;
+  if (q8) {
+    deal(items, cta_begin);
+    deal(wide, wide_begin);
   }
 
   std::stable_sort(xitems.begin(), xitems.end(), [](const ExtItem& a, const ExtItem& b) {
@@ -719,6 +791,10 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   h.n_xitems = (int32_t)xitems.size();
   h.off_cta = off; off = align256(off + cta_begin.size() * sizeof(int32_t));
   h.n_ctas = cta_begin.empty() ? 0 : (int32_t)cta_begin.size() - 1;
+  h.off_wide = off; off = align256(off + wide.size() * sizeof(DecItem));
+  h.off_wide_cta = off; off = align256(off + wide_begin.size() * sizeof(int32_t));
+  h.n_wide = (int32_t)wide.size();
+  h.n_wide_ctas = wide_begin.empty() ? 0 : (int32_t)wide_begin.size() - 1;
   h.max_refs = max_refs;
   const size_t tables = off;
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
@@ -735,6 +811,8 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   put(plan->blob, h.off_xrows, xrows);
   put(plan->blob, h.off_xsegs, xsegs);
   put(plan->blob, h.off_cta, cta_begin);
+  put(plan->blob, h.off_wide, wide);
+  put(plan->blob, h.off_wide_cta, wide_begin);
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 2;

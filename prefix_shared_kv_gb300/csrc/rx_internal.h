@@ -47,15 +47,14 @@ constexpr int kDecRows = 128;                              // (head, key) rows p
 constexpr int kDecStageBytes = 2 * kDecRows * kHeadDim * 2;   // K + V, 128 rows each
 constexpr size_t kDecSmemBytes = (size_t)kDecStages * kDecStageBytes + kDecMaxKeysPerItem * 4;
 
-// Decode over an 8-bit pool: items of the same form, cut for decode_q8_kernel.  Its kinds are
-// tiles of 8 query rows: kind 0 one (up to 8 rows), kind 1 two.  Eight consumer warps take a KV
-// head each, 32 keys a stage; a block holds the largest power of two of heads (at most 8) that
-// divides num_kv_heads, and with fewer than 8 heads the warps split a stage's keys (8 / heads ways).
-// A work unit's partial rows: [split][KV head][row].
+// Decode over an 8-bit pool: items of the same form, cut for decode_q8_kernel.  Narrow items have
+// up to kQ8MaxRows stacked query rows (kind 0: up to 8, kind 1: up to 16), wide ones (a table and
+// a launch of their own) up to kQ8MaxWideRows.  A block of a narrow item holds the largest power of two
+// of heads (at most 8) that divides num_kv_heads, of a wide item half of it (at least 1).  Eight
+// warps (narrow) or four pairs of warps (wide) take a head each, 32 keys a stage; with fewer heads
+// they split a stage's keys.  A work unit's partial rows: [split][KV head][row].
 constexpr int kQ8WarpKeys = 32;
-constexpr int kQ8MaxRows = 16;
-constexpr int kQ8MinStages = 8;
-constexpr int kQ8StageCost = 2, kQ8ItemCost = 3;  // planner: an item costs as much as 1.5 stages more
+constexpr int kQ8MaxRows = 16, kQ8MaxWideRows = 64;
 inline int q8_head_block_log2(int hkv) {
   return hkv % 8 == 0 ? 3 : hkv % 4 == 0 ? 2 : hkv % 2 == 0 ? 1 : 0;
 }
@@ -142,7 +141,10 @@ struct PlanHeader {
   int32_t max_refs;      // decode plans: the most partials of a request
   int32_t n_q8_tiles;    // extend plans for the 8-bit pool: Q8Tile table and expanded segments
   int64_t off_q8_tiles, off_q8_stage;
-  int64_t pad[10];
+  // decode plans for the 8-bit pool: wide items and their per-CTA lists
+  int64_t off_wide, off_wide_cta;
+  int32_t n_wide, n_wide_ctas;
+  int64_t pad[7];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
 
