@@ -2,14 +2,14 @@
 //
 // With codes kc, vc (e4m3) and scales ks, vs (fp32) of key j, and base-2 scores
 //   s_j = scale log2(e) ks_j (q . kc_j):     o = sum_j 2^s_j vs_j vc_j / sum_j 2^s_j.
-// The codes are exact in fp16, so both products run on the fp16 tensor cores with fp32 sums: a
-// query row is brought to fp16 by a power of two that puts its largest magnitude in [2^14, 2^15)
-// (what the conversion loses is below 2^-38 of that magnitude, and the power comes back in fp32).
-// The second product's weights are 2^(s_j - m') vs_j, m' a running reference for s_j + log2 vs_j:
-// at most 2^8 whatever the scales are, so fp16 holds them to 2^-11 of their value down to 2^-14,
-// and to 2^-25 below.  The softmax's sum has a reference m of its own.  Both only move (and O is only
-// rescaled) when some score of the warp's passes its reference by more than 2^8, which one vote per
-// step decides.
+// The codes are exact in fp16, so both products run on the fp16 tensor cores with fp32 sums: a warp's
+// query rows are brought to fp16 by a power of two that puts their largest magnitude in
+// [2^14, 2^15) (what the conversion loses is below 2^-39 of that magnitude, and the power comes back
+// in fp32).  With p_j = 2^(s_j - m), m a running reference of the row, the sum takes p_j and the
+// second product's weights are p_j vs_j c, c a power of two of the row that keeps them at 2^8 or
+// less whatever the scales are: fp16 holds them to 2^-11 of their value down to 2^-14, and to
+// 2^-25 below.  m and c only move (and O is only rescaled) when some p_j or weight of the warp's
+// passes 2^8, which one vote per step decides; until then a step needs no maximum across lanes.
 //
 // Work items are the bf16 decode's: a chunk of one table row's keys for a block of KV heads and
 // some stacked query rows (a shared prefix's members, or one request).  The queries are the narrow
@@ -208,60 +208,61 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
   const int rows = it.n_tok * p.gq;
 
   // Query fragments: position 2c + e of a 16-wide step holds d = 16 step + 4c + e, and 8 + 2c + e
-  // holds 16 step + 4c + 2 + e, as the conversion of four neighbouring codes leaves K.
+  // holds 16 step + 4c + 2 + e, as the conversion of four neighbouring codes leaves K.  The wide
+  // form keeps them in shared memory, written and read by the same lane.
   uint2 qf[WIDE ? 1 : 8][WIDE ? 1 : NT];
   uint2* sq = reinterpret_cast<uint2*>(smem + F::kOffQ + warp * F::kQWarp) + lane;
-  float qs[NT][2];  // scale_log2 and the row's power of two, for the columns 2c and 2c + 1
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = row0 + 8 * n + g;
-    uint2 x[8];
+  float qs;  // scale_log2 and the power of two
+  {
     uint32_t m = 0;
-    if (r < rows) {
-      const __nv_bfloat16* src =
-          p.q + ((int64_t)__ldg(p.rows + it.row_begin + r / p.gq) * p.hq + head * p.gq + r % p.gq) *
-                    kHeadDim + 4 * c;
+    auto row_ptr = [&](int n) {
+      const int r = row0 + 8 * n + g;
+      return r < rows ? reinterpret_cast<const uint2*>(
+                            p.q + ((int64_t)__ldg(p.rows + it.row_begin + r / p.gq) * p.hq +
+                                   head * p.gq + r % p.gq) * kHeadDim + 4 * c)
+                      : nullptr;
+    };
+    uint2 x[WIDE ? 1 : NT][8];
+    auto load = [&](const uint2* src, uint2 (&y)[8]) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = __ldg(reinterpret_cast<const uint2*>(src + 16 * k));
-    } else {
+      for (int k = 0; k < 8; ++k) {
+        y[k] = src ? __ldg(src + 4 * k) : make_uint2(0, 0);
+        m = __vmaxu2(m, __vmaxu2(y[k].x & 0x7fff7fffu, y[k].y & 0x7fff7fffu));
+      }
+    };
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = make_uint2(0, 0);
-    }
+    for (int n = 0; n < NT; ++n) load(row_ptr(n), x[WIDE ? 0 : n]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      m = __vmaxu2(m, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // biased exponent of the row's largest magnitude; a row below 2^-87 keeps 2^-87's power
+    for (int off = 1; off < 32; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    // biased exponent of the largest magnitude; rows below 2^-87 keep 2^-87's power
     const int e = max((int)(max(m & 0xffffu, m >> 16) >> 7), 40);
     const float up = __uint_as_float((uint32_t)(268 - e) << 23);
-    const float down = __uint_as_float((uint32_t)(e - 14) << 23);
+    qs = __uint_as_float((uint32_t)(e - 14) << 23) * p.scale_log2;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint2 y = make_uint2(pack_f16(__uint_as_float(x[k].x << 16) * up,
-                                          __uint_as_float(x[k].x & 0xffff0000u) * up),
-                                 pack_f16(__uint_as_float(x[k].y << 16) * up,
-                                          __uint_as_float(x[k].y & 0xffff0000u) * up));
-      if constexpr (WIDE)
-        sq[(k * NT + n) * 32] = y;  // read by this lane only
-      else
-        qf[k][n] = y;
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (WIDE) load(row_ptr(n), x[0]);  // (again, from the cache: fewer registers)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint2 v = x[WIDE ? 0 : n][k];
+        const uint2 y = make_uint2(pack_f16(__uint_as_float(v.x << 16) * up,
+                                            __uint_as_float(v.x & 0xffff0000u) * up),
+                                   pack_f16(__uint_as_float(v.y << 16) * up,
+                                            __uint_as_float(v.y & 0xffff0000u) * up));
+        if constexpr (WIDE)
+          sq[(k * NT + n) * 32] = y;
+        else
+          qf[k][n] = y;
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      qs[n][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j)) * p.scale_log2;
   }
 
   float o[8][NT][4];
-  // references of the sum and of the weights, 2^(m1 - m2), the sum (this lane's keys)
-  float m1[NT][2], m2[NT][2], cw[NT][2], l[NT][2];
+  // per column pair 2c, 2c + 1: -m, c, and this lane's part of the sum
+  uint64_t nm[NT], cw[NT], l[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      m1[n][j] = m2[n][j] = kUnset;
-      cw[n][j] = l[n][j] = 0.f;
-    }
+    nm[n] = f2_pack(-kUnset, -kUnset);
+    cw[n] = l[n] = 0ull;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
   }
@@ -306,74 +307,105 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
             }
           }
         }
-      // scales and masks (columns 2c + j; keys 16 t + 8 h + g); how far the scores pass the
-      // references
-      float vs[KT][2], lv[KT][2], over = kUnset;
+      // scales of keys 16 t + 8 h + g; a key past the item's has score -inf and weight 0
+      float kq[KT][2], vs[KT][2];
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int key = 16 * (t0 + t) + 8 * h + g;
-          const float ks = sc[key * HB];
+          kq[t][h] = sc[key * HB] * qs;
           vs[t][h] = sc[F::kRows + key * HB];
-          lv[t][h] = lg2(vs[t][h]);
+        }
+      if (16 * (t0 + KT) > left) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (16 * (t0 + t) + 8 * h + g >= left) {
+              kq[t][h] = 1.f;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                s[t][n][2 * h] = s[t][n][2 * h + 1] = -CUDART_INF_F;
+            }
+      }
+      uint32_t pt[KT][NT][2];  // P^T: columns are query rows, two keys a register
+      uint64_t add[NT];
+      auto weigh = [&]() {  // weights and sums under the present references; the largest
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) add[n] = 0ull;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float v = key < left ? s[t][n][2 * h + j] * ks * qs[n][j] : -CUDART_INF_F;
-              s[t][n][2 * h + j] = v;
-              over = fmax3(over, v - m1[n][j], v + lv[t][h] - m2[n][j]);
+            for (int h = 0; h < 2; ++h) {
+              float e0, e1, w0, w1;
+              f2_unpack(f2_fma(f2_pack(s[t][n][2 * h], s[t][n][2 * h + 1]),
+                               f2_pack(kq[t][h], kq[t][h]), nm[n]), e0, e1);
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              const uint64_t e = f2_pack(e0, e1);
+              add[n] = f2_add(add[n], e);
+              f2_unpack(f2_mul(f2_mul(e, f2_pack(vs[t][h], vs[t][h])), cw[n]), w0, w1);
+              top = fmax3(top, e0, e1);
+              top = fmax3(top, w0, w1);
+              pt[t][n][h] = pack_f16(w0, w1);
             }
-        }
-      if (__any_sync(0xffffffffu, over > 8.f)) {
+        return top;
+      };
+      if (__any_sync(0xffffffffu, weigh() > 256.f)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          float m[2], w[2], ls[2];
+          f2_unpack(nm[n], m[0], m[1]);
+          f2_unpack(cw[n], w[0], w[1]);
+          f2_unpack(l[n], ls[0], ls[1]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x1 = m1[n][j], x2 = m2[n][j];
+            const float m_old = -m[j];
+            const int ew = (int)(__float_as_uint(w[j]) >> 23) - 127;  // log2 c
+            float x1 = m_old, x2 = w[j] == 0.f ? kUnset : m_old - (float)ew;
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                x1 = fmaxf(x1, s[t][n][2 * h + j]);
-                x2 = fmaxf(x2, s[t][n][2 * h + j] + lv[t][h]);
+                const float v = s[t][n][2 * h + j] * kq[t][h];
+                x1 = fmaxf(x1, v);
+                x2 = fmaxf(x2, v + lg2(vs[t][h]));
               }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
               x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
               x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, off));
             }
-            l[n][j] *= fast_exp2(m1[n][j] - x1);
-            const float a2 = fast_exp2(m2[n][j] - x2);
+            // c = 2^en with weights of at most about 1; none while every V scale was 0
+            const int en = x2 == kUnset ? -127 : (int)rintf(fminf(fmaxf(x1 - x2, -126.f), 126.f));
+            ls[j] *= fast_exp2(m_old - x1);
+            const float a = w[j] == 0.f ? 0.f : fast_exp2(m_old - x1 + (float)(en - ew));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              o[i][n][j] *= a2;
-              o[i][n][2 + j] *= a2;
+              o[i][n][j] *= a;
+              o[i][n][2 + j] *= a;
             }
-            m1[n][j] = x1;
-            m2[n][j] = x2;
-            // (no key with a V scale yet: nothing to weigh; above 2^126 the weights themselves
-            // are below the smallest float)
-            cw[n][j] = x2 == kUnset ? 0.f : fast_exp2(fminf(x1 - x2, 126.f));
+            m[j] = -x1;
+            w[j] = __uint_as_float((uint32_t)(en + 127) << 23);
           }
+          nm[n] = f2_pack(m[0], m[1]);
+          cw[n] = f2_pack(w[0], w[1]);
+          l[n] = f2_pack(ls[0], ls[1]);
+        }
+        weigh();
       }
-      uint32_t pt[KT][NT][2];  // P^T: columns are query rows, two keys a register
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+      for (int n = 0; n < NT; ++n) {
+        l[n] = f2_add(l[n], add[n]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float w[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float e = fast_exp2(s[t][n][2 * h + j] - m1[n][j]);
-              l[n][j] += e;
-              w[j] = e * vs[t][h] * cw[n][j];
-            }
-            pt[t][n][h] = movm_t(pack_f16(w[0], w[1]));
-          }
+          for (int h = 0; h < 2; ++h) pt[t][n][h] = movm_t(pt[t][n][h]);
+      }
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -402,21 +434,24 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
   if (split * kQ8WarpKeys >= nkeys) return true;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
+    float m[2], w[2], ls[2];
+    f2_unpack(nm[n], m[0], m[1]);
+    f2_unpack(cw[n], w[0], w[1]);
+    f2_unpack(l[n], ls[0], ls[1]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1)
-        l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], off);
+      for (int off = 4; off < 32; off <<= 1) ls[j] += __shfl_xor_sync(0xffffffffu, ls[j], off);
       const int r = row0 + 8 * n + 2 * c + j;
       if (r >= rows) continue;
-      const bool none = l[n][j] == 0.f;
-      const float f = none ? 0.f : fast_exp2(m2[n][j] - m1[n][j]) / l[n][j];
+      const bool none = ls[j] == 0.f;
+      const float f = none || w[j] == 0.f ? 0.f : 1.f / w[j] / ls[j];
       const int64_t row = (int64_t)it.part + ((int64_t)split * p.hkv + head) * rows + r;
       float* dst = p.part_o + row * kHeadDim + 2 * g;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[i][n][j] * f, o[i][n][2 + j] * f);
-      if (g == 0) p.part_lse[row] = none ? -CUDART_INF_F : m1[n][j] + __log2f(l[n][j]);
+      if (g == 0) p.part_lse[row] = none ? -CUDART_INF_F : -m[j] + __log2f(ls[j]);
     }
   }
   return true;
