@@ -597,9 +597,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
 }
 
 template <int W>
-cudaError_t launch_merge(const Params& p, const uint8_t* base, const PlanHeader* h, void* o,
-                         float* lse, cudaStream_t stream) {
-  const int64_t tasks = (int64_t)h->batch * p.hq;
+cudaError_t launch_merge(const uint8_t* base, const PlanHeader* h, int32_t n, int hq, int gq,
+                         void* o, float* lse, cudaStream_t stream) {
+  const int64_t tasks = (int64_t)n * hq;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tasks + kMergeWarps / W - 1) / (kMergeWarps / W)));
   cfg.blockDim = dim3(32 * kMergeWarps);
@@ -609,11 +609,12 @@ cudaError_t launch_merge(const Params& p, const uint8_t* base, const PlanHeader*
   beside.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &beside;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_q8_kernel<W>, (const float*)p.part_o,
-                            (const float*)p.part_lse,
+  return cudaLaunchKernelEx(&cfg, merge_q8_kernel<W>,
+                            reinterpret_cast<const float*>(base + h->off_part_o),
+                            reinterpret_cast<const float*>(base + h->off_part_lse),
                             reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
-                            reinterpret_cast<const DecMergeRef*>(base + h->off_merge),
-                            (int)h->batch, p.hq, p.gq, static_cast<__nv_bfloat16*>(o), lse);
+                            reinterpret_cast<const DecMergeRef*>(base + h->off_merge), (int)n, hq,
+                            gq, static_cast<__nv_bfloat16*>(o), lse);
 }
 
 template <bool WIDE, int HBL>
@@ -694,13 +695,18 @@ int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
                    : launch_partials<false, 0>(p, h->n_ctas, s);
     if (e != cudaSuccess) return (int)e;
   }
-  if (h->batch > 0) {
-    // one warp a row up to 8 partials (all its reads in flight at once), two up to 32, else eight
-    e = h->max_refs <= 8    ? launch_merge<1>(p, base, h, o, lse, s)
-        : h->max_refs <= 32 ? launch_merge<2>(p, base, h, o, lse, s)
-                            : launch_merge<8>(p, base, h, o, lse, s);
-  }
-  return (int)e;
+  return h->batch > 0 ? launch_merge_q8(d, h, h->batch, o, lse, ws, stream) : 0;
+}
+
+int launch_merge_q8(const rx_kv_desc* d, const PlanHeader* h, int32_t n, void* o, float* lse,
+                    void* ws, void* stream) {
+  const uint8_t* base = static_cast<const uint8_t*>(ws);
+  const int hq = d->num_q_heads, gq = hq / d->num_kv_heads;
+  cudaStream_t s = (cudaStream_t)stream;
+  // one warp a row up to 8 partials (all its reads in flight at once), two up to 32, else eight
+  return (int)(h->max_refs <= 8    ? launch_merge<1>(base, h, n, hq, gq, o, lse, s)
+               : h->max_refs <= 32 ? launch_merge<2>(base, h, n, hq, gq, o, lse, s)
+                                   : launch_merge<8>(base, h, n, hq, gq, o, lse, s));
 }
 
 }  // namespace rx

@@ -97,7 +97,7 @@ constexpr int kQTile = 2 * kQHalf;     // 32 KiB
 constexpr int kKVHalf = kN * 128;      // one 64-column half of a 64-key K or V tile: 8 KiB
 constexpr int kKVTile = 2 * kKVHalf;   // 16 KiB
 constexpr int kScRing = 8;             // steps in the ring of scales (8-bit pool)
-constexpr int kScStep = 2 * kN * 4;    // K scales, then V scales, of a step's keys
+constexpr int kScStep = 2 * kN * 4 + 16;  // K scales, V scales and the NaN word of a step's keys
 // TMEM columns: S buffers S_A0, S_A1, S_B0, S_B1 of 64 columns from 0 (P_x(t), 64 bf16 a row, two
 // a column, over the upper half of S_x's buffer t % 2), O_A [256,384), O_B [384,512)
 constexpr uint32_t kTmemCols = 512;
@@ -344,7 +344,8 @@ static __device__ __forceinline__ void producer_q8(const ExtParams& p, uint32_t 
           const uint32_t e = gt % kScRing, sc = base + kOffSc + e * kScStep;
           mbar_expect_tx(bar + 8 * (B_SC_FULL + e), kScStep);
           bulk_copy(sc, src + kKVTile, 4 * kN, bar + 8 * (B_SC_FULL + e));
-          bulk_copy(sc + 4 * kN, src + kQ8BlockV + kKVTile, 4 * kN, bar + 8 * (B_SC_FULL + e));
+          bulk_copy(sc + 4 * kN, src + kQ8BlockV + kKVTile, kScStep - 4 * kN,
+                    bar + 8 * (B_SC_FULL + e));
         }
         src += (int64_t)p.hkv * kQ8BlockBytes;
       }
@@ -667,8 +668,12 @@ static __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const E
     uint64_t acc[2] = {0ull, 0ull};
     row_exp(sr, pk, acc, scales + 4 * kN);
     if constexpr (Q8) {
-      // a masked key's P is 0 whatever its V scale is (0 * NaN is not)
-      if (n_ok < kN) {
+      // a masked key's P is 0 whatever its V scale is (0 * NaN is not; the word says whether the
+      // step has such a scale: without it this loop cost 7 % on batches with many masked steps)
+      uint32_t nan = 0;
+      if (n_ok < kN)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(nan) : "r"(scales + 8 * kN) : "memory");
+      if (nan) {
 #pragma unroll
         for (int e = 0; e < kN; e += 2)
           pk[e >> 1] = e + 1 < n_ok ? pk[e >> 1] : e < n_ok ? pk[e >> 1] & 0xffffu : 0u;
@@ -1067,12 +1072,16 @@ int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   const int e = launch_expand_q8(d, kv, reinterpret_cast<const Q8Tile*>(base + h->off_q8_tiles),
                                  h->n_q8_tiles, base + h->off_q8_stage, status, stream);
   if (e) return e;
-  return launch_items<true>(d, reinterpret_cast<const ExtItem*>(base + h->off_items),
-                            reinterpret_cast<const ExtRow*>(base + h->off_rows),
-                            reinterpret_cast<const ExtSeg*>(base + h->off_segs), h->n_items,
-                            reinterpret_cast<const int32_t*>(base + h->off_cta), h->n_ctas, nullptr,
-                            nullptr, base + h->off_q8_stage, q, o, lse, nullptr, nullptr, status,
-                            stream);
+  // a plan whose tiles do not fill the GPU splits their keys: partial rows, and a merge
+  float* part_o = h->n_part_rows ? reinterpret_cast<float*>(base + h->off_part_o) : nullptr;
+  float* part_lse = h->n_part_rows ? reinterpret_cast<float*>(base + h->off_part_lse) : nullptr;
+  const int r = launch_items<true>(
+      d, reinterpret_cast<const ExtItem*>(base + h->off_items),
+      reinterpret_cast<const ExtRow*>(base + h->off_rows),
+      reinterpret_cast<const ExtSeg*>(base + h->off_segs), h->n_items,
+      reinterpret_cast<const int32_t*>(base + h->off_cta), h->n_ctas, nullptr, nullptr,
+      base + h->off_q8_stage, q, o, lse, part_o, part_lse, status, stream);
+  return !r && part_o ? launch_merge_q8(d, h, h->n_rows, o, lse, ws, stream) : r;
 }
 
 }  // namespace rx

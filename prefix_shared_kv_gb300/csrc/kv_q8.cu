@@ -33,6 +33,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// 32 bytes at once (the address 32-byte aligned), or as two halves.
+template <bool B32>
+__device__ __forceinline__ void ld32b(const uint4* p, uint4 (&x)[2]) {
+  if constexpr (B32) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x),
+                   "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
+                 : "l"(p));
+  } else {
+    x[0] = __ldcs(p);
+    x[1] = __ldcs(p + 1);
+  }
+}
+template <bool B32>
+__device__ __forceinline__ void st32b(uint4* p, const uint4 (&x)[2]) {
+  if constexpr (B32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0].x),
+                 "r"(x[0].y), "r"(x[0].z), "r"(x[0].w), "r"(x[1].x), "r"(x[1].y), "r"(x[1].z),
+                 "r"(x[1].w)
+                 : "memory");
+  } else {
+    p[0] = x[0];
+    p[1] = x[1];
+  }
+}
+
 // A position in the flat list of rows, moved on by a fixed stride without divisions.
 struct RowIter {
   int64_t row, token;
@@ -49,7 +75,7 @@ struct RowIter {
   }
 };
 
-template <int U>
+template <int U, bool B32>
 __global__ void __launch_bounds__(kThreads) store_q8_kernel(
     uint8_t* __restrict__ k_code, uint8_t* __restrict__ v_code, float* __restrict__ k_scale,
     float* __restrict__ v_scale, const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
@@ -76,8 +102,7 @@ __global__ void __launch_bounds__(kThreads) store_q8_kernel(
         const int64_t s = __ldg(slots + it.token);
         if (s >= 0 && s < pool_size) {
           dst[u] = s * hkv + it.head;
-          x[u][0] = __ldcs(src + it.row * 16 + 2 * l);
-          x[u][1] = __ldcs(src + it.row * 16 + 2 * l + 1);
+          ld32b<B32>(src + it.row * 16 + 2 * l, x[u]);
         }
       }
       it.step(stride, st_tokens, st_heads, hkv);
@@ -114,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) store_q8_kernel(
   }
 }
 
-template <int U>
+template <int U, bool B32>
 __global__ void __launch_bounds__(kThreads) load_q8_kernel(
     const uint8_t* __restrict__ k_code, const uint8_t* __restrict__ v_code,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale,
@@ -124,41 +149,51 @@ __global__ void __launch_bounds__(kThreads) load_q8_kernel(
   const uint8_t* code = is_v ? v_code : k_code;
   const float* scale = is_v ? v_scale : k_scale;
   uint4* out = is_v ? v_out : k_out;
-  const int l = threadIdx.x & 15;  // lane of the row: values 8 l .. 8 l + 7
-  const int64_t stride = (int64_t)gridDim.x * (kThreads / 16);
+  const int l = threadIdx.x & 7;  // lane of the row: values 16 l .. 16 l + 15
+  const int64_t stride = (int64_t)gridDim.x * (kThreads / 8);
   const int64_t st_tokens = stride / hkv;
   const int st_heads = (int)(stride - st_tokens * hkv);
-  RowIter it((int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16, hkv);
-  while (it.row < n_rows) {
-    uint2 c[U];
-    float sc[U];
-    const int64_t first = it.row;
+  RowIter it((int64_t)blockIdx.x * (kThreads / 8) + threadIdx.x / 8, hkv);
+  int64_t src[U];  // rows of the pool of the next U, -1: none, or outside the pool (zeros)
+  auto fetch = [&]() {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      c[u] = make_uint2(0, 0);
-      sc[u] = 0.f;
+      src[u] = -1;
       if (it.row < n_rows) {
         const int64_t s = __ldg(slots + it.token);
-        if (s >= 0 && s < pool_size) {  // a slot outside the pool reads as zeros
-          const int64_t r = s * hkv + it.head;
-          c[u] = __ldg(reinterpret_cast<const uint2*>(code + r * kHeadDim) + l);
-          sc[u] = __ldg(scale + r);
-        }
+        if (s >= 0 && s < pool_size) src[u] = s * hkv + it.head;
       }
       it.step(stride, st_tokens, st_heads, hkv);
     }
+  };
+  int64_t first = it.row;
+  fetch();
+  for (; first < n_rows; first += U * stride) {
+    uint4 c[U];
+    float sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      c[u] = make_uint4(0, 0, 0, 0);
+      sc[u] = 0.f;
+      if (src[u] >= 0) {
+        c[u] = __ldg(reinterpret_cast<const uint4*>(code + src[u] * kHeadDim) + l);
+        sc[u] = __ldg(scale + src[u]);
+      }
+    }
+    fetch();  // the next rows' slots, behind this round's codes
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t row = first + u * stride;
       if (row >= n_rows) break;
-      uint32_t w[4];
+      const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+      uint32_t y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = ((i < 2 ? c[u].x : c[u].y) >> (16 * (i & 1))) & 0xffffu;
-        const float2 f = e4m3x2_to_f32(pair);
-        w[i] = pack_bf16(f.x * sc[u], f.y * sc[u]);
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = e4m3x2_to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+        y[i] = pack_bf16(f.x * sc[u], f.y * sc[u]);
       }
-      __stcs(out + row * 16 + l, make_uint4(w[0], w[1], w[2], w[3]));
+      const uint4 o[2] = {make_uint4(y[0], y[1], y[2], y[3]), make_uint4(y[4], y[5], y[6], y[7])};
+      st32b<B32>(out + row * 16 + 2 * l, o);
     }
   }
 }
@@ -181,10 +216,11 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
 }
 
 // The expanded segments that the tensor-core extend kernel reads (layout at Q8Tile).  One CTA per
-// tile of 64 keys and group of up to eight KV heads: a lane turns 16 codes of a row of K and of V
+// tile of 64 keys and group of up to four KV heads: a lane turns 16 codes of a row of K and of V
 // into two 16-byte chunks of the operand's image; a row's codes are read by eight neighbouring
 // lanes, neighbouring heads of a key behind one another.  Moves 128 + 256 bytes a row.
-constexpr int kExpandHeads = 8;
+// (Heads a CTA: 2, 4 and 8 within 1 %, 16 2 % slower on 32 heads.)
+constexpr int kExpandHeads = 4;
 __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     const uint8_t* __restrict__ k_code, const uint8_t* __restrict__ v_code,
     const float* __restrict__ k_scale, const float* __restrict__ v_scale,
@@ -193,6 +229,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     int32_t* status) {
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int32_t s_slot[kAttnKeys];
+  __shared__ uint32_t s_nan[kExpandHeads];
   const Q8Tile tile = tiles[blockIdx.x];
   const int head0 = blockIdx.y * kExpandHeads, nh = min(kExpandHeads, hkv - head0);
   if (threadIdx.x < kAttnKeys) {
@@ -206,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     }
     s_slot[threadIdx.x] = s;
   }
+  if (threadIdx.x < kExpandHeads) s_nan[threadIdx.x] = 0;
   __syncthreads();
   uint8_t* blocks = stage + ((int64_t)blockIdx.x * hkv + head0) * kQ8BlockBytes;
   for (int i = threadIdx.x; i < kAttnKeys * nh; i += kThreads) {
@@ -215,7 +253,9 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     float* sc = reinterpret_cast<float*>(blocks + (int64_t)h * kQ8BlockBytes + kQ8BlockV) -
                 kAttnKeys + key;
     sc[0] = ok ? __ldg(k_scale + row) * scale_log2 : 0.f;
-    sc[kQ8BlockV / 4] = ok ? __ldg(v_scale + row) : 0.f;
+    const float v = ok ? __ldg(v_scale + row) : 0.f;
+    sc[kQ8BlockV / 4] = v;
+    if (isnan(v)) s_nan[h] = 1;  // (every writer writes the same)
   }
   const int n = kAttnKeys * nh * 8;
   constexpr int U = 4;
@@ -242,16 +282,21 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
       const int c = i & 7, f = i >> 3, key = f / nh, h = f - key * nh;
       // chunks 2c and 2c + 1 of the row: half c / 4, swizzled by the row's low three bits
       uint8_t* dst = blocks + (int64_t)h * kQ8BlockBytes + (c >> 2) * (kAttnKeys * 128) + key * 128;
-      const int c0 = (((2 * c) & 7) ^ (key & 7)) << 4, c1 = (((2 * c + 1) & 7) ^ (key & 7)) << 4;
+      dst += (((2 * c) & 6) ^ (key & 6)) << 4;  // the two chunks' 32 bytes; an odd row swaps them
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const uint2 a = e4m3x4_to_bf16(x[u][v].x), b = e4m3x4_to_bf16(x[u][v].y);
         const uint2 e = e4m3x4_to_bf16(x[u][v].z), g = e4m3x4_to_bf16(x[u][v].w);
-        *reinterpret_cast<uint4*>(dst + v * kQ8BlockV + c0) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(dst + v * kQ8BlockV + c1) = make_uint4(e.x, e.y, g.x, g.y);
+        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, g.x, g.y);
+        const uint4 y[2] = {key & 1 ? hi : lo, key & 1 ? lo : hi};
+        st32b<true>(reinterpret_cast<uint4*>(dst + v * kQ8BlockV), y);
       }
     }
   }
+  __syncthreads();
+  if ((int)threadIdx.x < nh)
+    *reinterpret_cast<uint32_t*>(blocks + (int64_t)threadIdx.x * kQ8BlockBytes + 2 * kQ8BlockV) =
+        s_nan[threadIdx.x];
 }
 
 int sm_count() {
@@ -262,6 +307,20 @@ int sm_count() {
   return sms;
 }
 
+// Launch shapes (GB300, K and V each).  Many rows: four a thread in flight and two CTAs per SM;
+// 13,064 tokens x 32 heads stored take 53.5 us so, 54.9 with two rows a thread, 58.4 with four CTAs
+// per SM; 32,003 x 32 read back 124.7 us, 129.6 with four CTAs, 126.6 with two rows and four CTAs.
+// Few rows, up to what the GPU holds at once with one row a thread: one, and as many CTAs as that
+// makes; 40 tokens x 32 heads stored take 1.9 us so, 3.4 with four rows a thread.
+constexpr int kManyRows = 4, kManyCtas = 2;
+bool few_rows(int64_t rows, int sms) { return rows <= (int64_t)sms * (2048 / kThreads / 2) * (kThreads / 8); }
+
+// One x column per kThreads / 8 * u rows, at most `most`; y: K, V.
+dim3 rows_grid(int64_t rows, int u, int64_t most) {
+  const int64_t per = (int64_t)(kThreads / 8) * u, blocks = (rows + per - 1) / per;
+  return dim3((unsigned)(blocks < most ? blocks : most), 2);
+}
+
 }  // namespace
 
 int launch_store_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const void* k_new,
@@ -270,16 +329,16 @@ int launch_store_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const void* k_ne
   const int64_t rows = n * d->num_kv_heads;
   const int sms = sm_count();
   if (sms == 0) return (int)cudaGetLastError();
-  constexpr int kRows = kThreads / 8;
+  const bool b32 = ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 31) == 0;
   auto run = [&](auto kernel, int u) {
-    const int64_t blocks = (rows + (int64_t)kRows * u - 1) / ((int64_t)kRows * u);
-    const dim3 grid((unsigned)(blocks < 4LL * sms ? blocks : 4LL * sms), 2);
-    kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
+    kernel<<<rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), kThreads, 0, (cudaStream_t)stream>>>(
         (uint8_t*)kv->k_code, (uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, (const uint4*)k_new,
         (const uint4*)v_new, slots, rows, d->num_kv_heads, d->pool_size);
     return (int)cudaGetLastError();
   };
-  return run(store_q8_kernel<4>, 4);
+  if (few_rows(rows, sms)) return b32 ? run(store_q8_kernel<1, true>, 1) : run(store_q8_kernel<1, false>, 1);
+  return b32 ? run(store_q8_kernel<kManyRows, true>, kManyRows)
+             : run(store_q8_kernel<kManyRows, false>, kManyRows);
 }
 
 int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* slots, int64_t n,
@@ -288,16 +347,16 @@ int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* sl
   const int64_t rows = n * d->num_kv_heads;
   const int sms = sm_count();
   if (sms == 0) return (int)cudaGetLastError();
-  constexpr int kRows = kThreads / 16;
+  const bool b32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   auto run = [&](auto kernel, int u) {
-    const int64_t blocks = (rows + (int64_t)kRows * u - 1) / ((int64_t)kRows * u);
-    const dim3 grid((unsigned)(blocks < 4LL * sms ? blocks : 4LL * sms), 2);
-    kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
+    kernel<<<rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), kThreads, 0, (cudaStream_t)stream>>>(
         (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, slots,
         (uint4*)k_out, (uint4*)v_out, rows, d->num_kv_heads, d->pool_size);
     return (int)cudaGetLastError();
   };
-  return run(load_q8_kernel<4>, 4);
+  if (few_rows(rows, sms)) return b32 ? run(load_q8_kernel<1, true>, 1) : run(load_q8_kernel<1, false>, 1);
+  return b32 ? run(load_q8_kernel<kManyRows, true>, kManyRows)
+             : run(load_q8_kernel<kManyRows, false>, kManyRows);
 }
 
 int launch_expand_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const Q8Tile* tiles, int32_t n_tiles,

@@ -371,8 +371,10 @@ rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches) {
   // the same conditions the launchers test: extend -- the tensor-core kernel when there are
   // items; decode -- the tensor-core kernel for its shared-prefix units, the mma.sync partial
   // kernel for the others, and the merge whenever there are requests
-  // (an extend over an 8-bit pool expands the plan's keys in a kernel of its own first)
-  *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3))
+  // (an extend over an 8-bit pool expands the plan's keys in a kernel of its own first, and merges
+  // when its tiles' keys are split)
+  *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3) +
+                                                   (h.n_part_rows > 0))
                               : (h.n_xitems > 0) + (h.n_wide > 0) + (h.n_items > 0) + (h.batch > 0);
   return RX_OK;
 }
@@ -979,6 +981,66 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   for (int b = 0; b < batch; ++b)
     if (grp[b] < 0 && extend_len[b] > 0) emit_unit(std::vector<int>{b}, 0);
 
+  // 8-bit pool: each distinct segment (table row, first key) gets tiles of kAttnKeys keys, as many
+  // as its longest use needs; the segments of the items then refer to their first tile.
+  const bool q8 = plan->kv_next == RX_KV_E4M3;
+  std::vector<Q8Tile> tiles8;
+  std::unordered_map<int64_t, std::pair<int32_t, int32_t>> stage;  // -> (longest end, first tile)
+  auto stage_of = [&](const ExtSeg& sg) -> std::pair<int32_t, int32_t>& {
+    return stage[(int64_t)sg.kv_row << 32 | (uint32_t)sg.k_begin];
+  };
+  if (q8) {
+    for (const Unit& un : units)
+      for (const Tile& tl : un.tiles)
+        for (const ExtSeg& sg : tl.segs)
+          stage_of(sg) = {std::max(stage_of(sg).first, sg.k_end), -1};
+    for (const Unit& un : units)
+      for (const Tile& tl : un.tiles)
+        for (const ExtSeg& sg : tl.segs) {
+          auto& w = stage_of(sg);
+          if (w.second >= 0) continue;
+          if ((int64_t)tiles8.size() + attn_steps(w.first - sg.k_begin) > (int64_t)INT32_MAX / 2)
+            return fail(RX_ERR_RANGE, "plan too large");
+          w.second = (int32_t)tiles8.size();
+          for (int k = sg.k_begin; k < w.first; k += kAttnKeys)
+            tiles8.push_back({sg.kv_row, k, std::min(kAttnKeys, w.first - k), 0});
+        }
+  }
+  // 8-bit pool: when the pairs of tiles below would leave SMs without work, the items are single
+  // tiles, and the steps of each tile are split over as many items as there are SMs for; such
+  // items leave partial rows, which a merge combines.  (In the units of attn_cost: writing a tile's
+  // partial rows costs about a step, the merge about 3 us.)  0: no split.
+  int32_t split_steps = 0;
+  auto tile_steps = [](const Tile& tl) {
+    int32_t n = 0;
+    for (const ExtSeg& sg : tl.segs) n += attn_steps(sg.k_end - sg.k_begin);
+    return n;
+  };
+  if (q8) {
+    const int64_t sms = plan_sm_count();
+    int64_t n_pairs = 0, n_tiles = 0, total = 0, most = 0;
+    for (const Unit& un : units) {
+      n_pairs += (int64_t)(un.tiles.size() + 1) / 2 * hkv;
+      n_tiles += (int64_t)un.tiles.size() * hkv;
+      for (const Tile& tl : un.tiles) {
+        total += (int64_t)tile_steps(tl) * hkv;
+        most = std::max<int64_t>(most, tile_steps(tl));
+      }
+    }
+    if (n_tiles > 0 && n_pairs < sms && n_tiles <= sms) {
+      int64_t c = std::max<int64_t>(2, (total + sms - 1) / sms);
+      auto count = [&](int64_t steps) {
+        int64_t n = 0;
+        for (const Unit& un : units)
+          for (const Tile& tl : un.tiles) n += (tile_steps(tl) + steps - 1) / steps * hkv;
+        return n;
+      };
+      while (c < most && count(c) > sms) ++c;
+      // a pair walks at least its longer tile, at the price of a two-tile step
+      if (c < most && 11 * c + 14 + 41 < 14 * most) split_steps = (int32_t)c;
+    }
+  }
+
   // Pair consecutive tiles of a unit (similar cost after the sort) into one item; the pair walks
   // the union of the two segment lists (same owner: the longer range).  An odd last tile is
   // paired with an empty one.
@@ -1050,6 +1112,73 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
                          return attn_cost(a) > attn_cost(b);
                        });
   }
+  // The items refer to the expanded tiles, or, split, are made anew.
+  std::vector<std::vector<DecMergeRef>> refs(split_steps ? cu[batch] : 0);
+  int64_t npart = 0;
+  if (q8 && !split_steps) {
+    for (ExtSeg& sg : segs) sg.kv_row = stage_of(sg).second;
+  } else if (q8) {
+    items.clear();
+    segs.clear();
+    for (const Unit& un : units)
+      for (const Tile& tl : un.tiles) {
+        const int32_t steps = tile_steps(tl), parts = (steps + split_steps - 1) / split_steps;
+        const int32_t per = (steps + parts - 1) / parts;
+        size_t at = 0;
+        int32_t k0 = tl.segs[0].k_begin;
+        while (at < tl.segs.size()) {
+          ExtItem it;
+          std::memset(&it, 0, sizeof it);
+          it.row_begin[0] = tl.row_begin;
+          it.n_tok[0] = tl.n_tok;
+          it.seg_begin = (int32_t)segs.size();
+          for (int32_t left = per; left > 0 && at < tl.segs.size();) {
+            const ExtSeg& sg = tl.segs[at];
+            const int32_t n = std::min(left, attn_steps(sg.k_end - k0));
+            const int32_t end = std::min(sg.k_end, k0 + n * kAttnKeys);
+            segs.push_back({stage_of(sg).second + (k0 - sg.k_begin) / kAttnKeys, k0, end, sg.owner});
+            it.n_steps += n;
+            left -= n;
+            k0 = end;
+            if (k0 >= sg.k_end && ++at < tl.segs.size()) k0 = tl.segs[at].k_begin;
+          }
+          it.n_seg = (int32_t)segs.size() - it.seg_begin;
+          // the rows that see one of the item's keys take its partial result
+          for (int i = 0; i < tl.n_tok; ++i) {
+            const ExtRow& row = rows[tl.row_begin + i];
+            bool sees = false;
+            for (int j = 0; j < it.n_seg && !sees; ++j) {
+              const ExtSeg& sg = segs[it.seg_begin + j];
+              sees = (sg.owner < 0 || sg.owner == row.owner) && sg.k_begin < row.kmax;
+            }
+            if (sees)
+              refs[row.q_row].push_back({(int32_t)npart, tl.n_tok * gq, i * gq, 0});
+          }
+          for (int h = 0; h < hkv; ++h) {
+            it.kv_head = h;
+            it.part[0] = (int32_t)(npart + (int64_t)h * tl.n_tok * gq);
+            items.push_back(it);
+          }
+          npart += (int64_t)hkv * tl.n_tok * gq;
+          if (npart > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
+        }
+      }
+  }
+  if (q8) {
+    key_reads = 0;  // the pool is read by the expansion only
+    for (const Q8Tile& t : tiles8) key_reads += (int64_t)t.n_keys * hkv;
+  }
+  std::vector<int32_t> midx;
+  std::vector<DecMergeRef> mref;
+  int32_t max_refs = 0;
+  if (split_steps) {
+    midx.push_back(0);
+    for (const auto& r : refs) {
+      mref.insert(mref.end(), r.begin(), r.end());
+      midx.push_back((int32_t)mref.size());
+      max_refs = std::max(max_refs, (int32_t)r.size());
+    }
+  }
   if (items.size() > (size_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
   std::vector<int32_t> cta_begin;
   if (pair_kernel) {
@@ -1116,32 +1245,6 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     items.swap(by_cta);
   }
 
-  // 8-bit pool: each distinct segment (table row, first key) gets tiles of kAttnKeys keys, as many
-  // as its longest use needs, and the segments refer to their first tile
-  std::vector<Q8Tile> tiles8;
-  if (plan->kv_next == RX_KV_E4M3) {
-    std::unordered_map<int64_t, std::pair<int32_t, int32_t>> where;  // -> (longest end, first tile)
-    auto key_of = [](const ExtSeg& sg) { return (int64_t)sg.kv_row << 32 | (uint32_t)sg.k_begin; };
-    for (const ExtSeg& sg : segs) {
-      auto& w = where[key_of(sg)];
-      w.first = std::max(w.first, sg.k_end);
-      w.second = -1;
-    }
-    for (ExtSeg& sg : segs) {
-      auto& w = where[key_of(sg)];
-      if (w.second < 0) {
-        if ((int64_t)tiles8.size() + attn_steps(w.first - sg.k_begin) > (int64_t)INT32_MAX / 2)
-          return fail(RX_ERR_RANGE, "plan too large");
-        w.second = (int32_t)tiles8.size();
-        for (int k = sg.k_begin; k < w.first; k += kAttnKeys)
-          tiles8.push_back({sg.kv_row, k, std::min(kAttnKeys, w.first - k), 0});
-      }
-      sg.kv_row = w.second;
-    }
-    key_reads = 0;  // the pool is read by the expansion only
-    for (const Q8Tile& t : tiles8) key_reads += (int64_t)t.n_keys * hkv;
-  }
-
   PlanHeader h;
   std::memset(&h, 0, sizeof h);
   h.magic = kPlanMagic;
@@ -1161,8 +1264,13 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   h.n_ctas = cta_begin.empty() ? 0 : (int32_t)cta_begin.size() - 1;
   h.off_q8_tiles = off; off = align256(off + tiles8.size() * sizeof(Q8Tile));
   h.n_q8_tiles = (int32_t)tiles8.size();
-  h.off_merge_idx = h.off_merge = h.off_part_o = h.off_part_lse = off;
+  h.off_merge_idx = off; off = align256(off + midx.size() * 4);
+  h.off_merge = off; off = align256(off + mref.size() * sizeof(DecMergeRef));
+  h.max_refs = max_refs;
   plan->blob.assign(off, 0);
+  h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
+  h.off_part_lse = off; off = align256(off + (size_t)npart * 4);
+  h.n_part_rows = npart;
   h.off_q8_stage = off; off = align256(off + tiles8.size() * (size_t)hkv * kQ8BlockBytes);
   h.total_bytes = off;
   std::memcpy(plan->blob.data(), &h, sizeof h);
@@ -1171,6 +1279,8 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
   put(plan->blob, h.off_segs, segs);
   put(plan->blob, h.off_cta, cta_begin);
   put(plan->blob, h.off_q8_tiles, tiles8);
+  put(plan->blob, h.off_merge_idx, midx);
+  put(plan->blob, h.off_merge, mref);
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 1;

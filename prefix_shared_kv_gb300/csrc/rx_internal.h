@@ -88,8 +88,8 @@ constexpr int kPairKeys = 128;
 // expanded into the workspace by a kernel of their own; ExtSeg::kv_row is then the segment's first
 // tile (its step i reads tile kv_row + i).  Block (tile, KV head), at tile * Hkv + head: the K
 // operand's shared-memory image (bf16 codes, two 64-column halves of 128-byte-swizzled rows), the
-// keys' K scales times softmax_scale * log2(e), the V operand's image, the keys' V scales.  Keys
-// past the segment are zeros with scale 0.
+// keys' K scales times softmax_scale * log2(e), the V operand's image, the keys' V scales, and a
+// word that is not 0 if one of the V scales is NaN.  Keys past the segment are zeros with scale 0.
 struct Q8Tile {
   int32_t kv_row;        // req_to_token row
   int32_t k_begin;
@@ -97,7 +97,7 @@ struct Q8Tile {
   int32_t pad;
 };
 constexpr int kQ8BlockV = kAttnKeys * kHeadDim * 2 + kAttnKeys * 4;  // offset of V in a block
-constexpr int kQ8BlockBytes = 2 * kQ8BlockV;
+constexpr int kQ8BlockBytes = 2 * kQ8BlockV + 128;
 
 // Two row tiles (A, B) of the same KV head that walk the same key segments: every K/V step feeds
 // 256 query rows.  Tile B may be empty (n_tok[1] == 0: the CTA runs tile A alone).  The same
@@ -138,7 +138,7 @@ struct PlanHeader {
   int64_t off_cta;
   int32_t n_ctas;
   int32_t kv_type;       // RX_KV_BF16 or RX_KV_E4M3: the pool the plan's calls read
-  int32_t max_refs;      // decode plans: the most partials of a request
+  int32_t max_refs;      // the most partials of a request (decode) or row (extend, 8-bit pool)
   int32_t n_q8_tiles;    // extend plans for the 8-bit pool: Q8Tile table and expanded segments
   int64_t off_q8_tiles, off_q8_stage;
   // decode plans for the 8-bit pool: wide items and their per-CTA lists
@@ -176,6 +176,10 @@ int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                   void* stream);
 int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
                      void* o, float* lse, void* ws, void* stream);
+// The merge of a plan's partial rows (merge tables and partials of `ws`) into rows 0 .. n - 1 of o and
+// lse; launched beside the kernel before it, whose end it waits for.
+int launch_merge_q8(const rx_kv_desc* d, const PlanHeader* h, int32_t n, void* o, float* lse,
+                    void* ws, void* stream);
 // The expanded segments of an extend plan for the 8-bit pool (see Q8Tile), written to `stage`.
 int launch_expand_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const Q8Tile* tiles, int32_t n_tiles,
                      void* stage, int32_t* status, void* stream);

@@ -530,6 +530,23 @@ def test_extend_long_prefix(cuda):
     check_extend(pool, q, o, lse, prefix, new)
 
 
+@pytest.mark.parametrize("hq,hkv,prefix,new", [
+    (8, 2, [1000] * 4, [40] * 4), (32, 8, [16000], [4]), (1, 1, [5000, 3], [1, 1]),
+    (6, 3, [2111, 77, 600], [9, 33, 1]), (8, 1, [4096], [17]), (2, 2, [0], [900])])
+def test_extend_small_batches_split_their_keys(cuda, hq, hkv, prefix, new):
+    rng, pool, _, _ = extend_case(cuda, 31 + hq, hq, hkv, prefix, new)
+    q, o, lse, ws = run_extend(pool, rng, prefix, new)
+    check_extend(pool, q, o, lse, prefix, new)
+    assert rx.read_status(ws) == rx.RX_OK
+
+
+def test_extend_small_batches_with_a_shared_prefix_split_their_keys(cuda):
+    prefix, new = [1500, 1500, 1530, 1500, 20], [3, 30, 1, 90, 2]
+    rng, pool, grp, gpl = extend_case(cuda, 41, 8, 2, prefix, new, [(range(4), 1500)])
+    q, o, lse, _ = run_extend(pool, rng, prefix, new, grp, gpl)
+    check_extend(pool, q, o, lse, prefix, new)
+
+
 def test_extend_every_code_and_scale(cuda):
     """Codes of every value (subnormal ones too) and scales over 2^60."""
     prefix, new = [254], [64]

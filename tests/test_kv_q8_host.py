@@ -184,7 +184,7 @@ def test_decode_plan_checks_are_those_of_the_bf16_pool(librx):
 
 def test_extend_plan_for_the_8_bit_pool_reads_each_distinct_key_once(librx):
     """A group's prefix is expanded once for all its members and tiles, a request's own keys once;
-    the workspace holds them: 64-key blocks of two 16 KiB images and two rows of scales."""
+    the workspace holds them: 64-key blocks of two 16 KiB images, two rows of scales and a word."""
     hkv, gp = 4, 300
     desc = _desc(16, hkv, pool=1 << 20, rows=64, stride=4096)
     new = [100, 1, 700, 0, 40]
@@ -195,8 +195,23 @@ def test_extend_plan_for_the_8_bit_pool_reads_each_distinct_key_once(librx):
     own = 100 + 65 + 700 + 240
     assert plan.key_reads() == (gp + own) * hkv
     tiles = sum(-(-n // 64) for n in (gp, 100, 65, 700, 240))
-    blocks = tiles * hkv * (2 * 64 * 256 + 2 * 64 * 4)
-    assert blocks <= plan.workspace_size() <= blocks + 65536
+    blocks = tiles * hkv * (2 * 64 * 256 + 2 * 64 * 4 + 128)
+    # (and, the batch being small, at most one partial tile of 128 rows per SM)
+    assert blocks <= plan.workspace_size() <= blocks + 160 * 128 * 516 + 65536
     bf = rx.Plan()
     rx.extend_plan(bf, desc, [0, 1, 2, 3, 4], prefix, new, [0, 0, 0, 0, -1], [gp])
     assert bf.workspace_size() < 65536 and bf.launches() == 1
+
+
+def test_extend_plan_splits_the_keys_of_a_batch_too_small_for_the_gpu(librx):
+    """Four requests of 40 new tokens on 1,000 cached ones: five tiles a head would leave most SMs
+    idle, so the tiles' keys are split and a merge is launched; a batch that fills the GPU is not."""
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    desc = _desc(8, 2, pool=1 << 20, rows=64, stride=4096)
+    rx.extend_plan(plan, desc, [0, 1, 2, 3], [1000] * 4, [40] * 4, [0] * 4, [1000])
+    assert plan.launches() == 3 and plan.rows() == 160
+    assert plan.key_reads() == (1000 + 160) * 2
+    desc = _desc(32, 32, pool=1 << 20, rows=64, stride=4096)
+    rx.extend_plan(plan, desc, np.arange(32), [1000] * 32, [200] * 32)
+    assert plan.launches() == 2
