@@ -24,8 +24,11 @@
 //               pool is flagged and read as zeros.
 // Two forms.  Narrow items have up to 16 rows: eight heads a block, queries in registers, three
 // stages.  Wide ones have up to 64: a head's rows go to two warps (32 each), four heads a block;
-// the O tile alone takes 128 registers, so the queries lie in shared memory as fragments, a step
-// is 16 keys, and the producers hand registers to the consumers.
+// the O tile alone takes 128 registers, so the queries lie in shared memory as fragments and the
+// producers hand registers to the consumers.  (On 16 x 16 requests with 64 rows per KV head and
+// 16,000 shared keys, whole call: 278 us; 16-key steps, which halve the independent products, 294
+// us; 224 or 216 registers for the consumers, with spills, 288 and 306 us; the references in shared
+// memory instead of spills, 284 us.)
 // A persistent CTA per SM runs the list of items that the planner gave it.  Each item leaves
 // normalised fp32 partial rows and base-2 log-sum-exps, which a last kernel merges.  The kernels are
 // chained by programmatic dependent launch: the narrow one starts as SMs come free of the wide
@@ -67,7 +70,7 @@ constexpr int kWarps = 8;        // consumers
 constexpr int kProducers = 128;  // threads
 constexpr int kThreads = 32 * kWarps + kProducers;
 // Registers: the launch's 168 a thread; the wide form moves them to its consumers.
-constexpr int kRegsLaunch = 168, kRegsConsumer = 216, kRegsProducer = 72;
+constexpr int kRegsLaunch = 168, kRegsConsumer = 232, kRegsProducer = 40;
 static_assert(2 * kRegsConsumer + kRegsProducer == 3 * kRegsLaunch, "register split");
 constexpr int kNoKey = INT32_MIN;  // past an item's keys
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -197,7 +200,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
                                          uint8_t* smem, uint32_t& gs, volatile int* abort) {
   using F = Form<WIDE, HBL>;
   constexpr int HB = F::HB, NK = F::NK;
-  constexpr int KT = WIDE ? 1 : 2;  // 16-key tiles of a step
+  constexpr int KT = kQ8WarpKeys / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int kw = warp % (kWarps / F::kRowWarps);  // the warp's 32-key run of a stage
@@ -277,9 +280,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
     const uint32_t vb = kb + F::kHalf;
     const float* sc = reinterpret_cast<const float*>(smem + st * F::kStageBytes + F::kOffScale) +
                       split * kQ8WarpKeys * HB + (kw & (HB - 1));
-#pragma unroll 1
-    for (int t0 = 0; t0 < 2; t0 += KT) {
-      if (16 * t0 >= left) break;
+    if (left > 0) {
       float s[KT][NT][4];
 #pragma unroll
       for (int t = 0; t < KT; ++t)
@@ -290,7 +291,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           uint32_t x[4];
-          const int r = 16 * (t0 + t) + (lane & 15);
+          const int r = 16 * t + (lane & 15);
           ldsm_x4(kb + row_off(r, 2 * k2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -313,16 +314,16 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = 16 * (t0 + t) + 8 * h + g;
+          const int key = 16 * t + 8 * h + g;
           kq[t][h] = sc[key * HB] * qs;
           vs[t][h] = sc[F::kRows + key * HB];
         }
-      if (16 * (t0 + KT) > left) {
+      if (left < kQ8WarpKeys) {
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (16 * (t0 + t) + 8 * h + g >= left) {
+            if (16 * t + 8 * h + g >= left) {
               kq[t][h] = 1.f;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
@@ -411,7 +412,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
 #pragma unroll
         for (int i2 = 0; i2 < 4; ++i2) {
           uint32_t x[4];
-          const int r = 16 * (t0 + t) + (lane & 15);
+          const int r = 16 * t + (lane & 15);
           ldsm_x4_t(vb + row_off(r, 2 * i2 + (lane >> 4)), x[0], x[1], x[2], x[3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
