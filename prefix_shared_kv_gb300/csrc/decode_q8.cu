@@ -39,6 +39,7 @@
 
 #include <atomic>
 
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "rx_internal.h"
 #include "tc.cuh"
@@ -472,7 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
     *abort = 0;
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;");
+  // A narrow kernel behind a wide one starts beside it: the wide one's CTAs have all passed this
+  // wait by then, so what came before the call is complete.
+  if (WIDE || !p.after_wide) wait_for_predecessors();
+  let_successors_start();
   if (threadIdx.x >= 32 * kWarps) {
     if constexpr (WIDE) tc::regs_dec<kRegsProducer>();
     producer<WIDE, HBL>(p, base, abort);
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
   }
   // the merge behind this kernel waits for this one only
   if constexpr (!WIDE)
-    if (p.after_wide) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (p.after_wide) wait_for_predecessors();
 }
 
 // W warps per (request, query head), W from the longest list of partials: warp w takes partials
@@ -517,7 +521,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q8_kernel(
   const int r_begin = merge_idx[b], n = live ? merge_idx[b + 1] - r_begin : 0;
   float mx = -CUDART_INF_F, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete behind it
+  wait_for_predecessors();  // the partials are complete
+  let_successors_start();
   // per chunk the lanes fetch one reference and log-sum-exp each, so every weight is known before
   // any row is read and the row reads are independent of one another
   for (int c0 = w; c0 < n; c0 += 32 * W) {
@@ -601,21 +606,14 @@ template <int W>
 cudaError_t launch_merge(const uint8_t* base, const PlanHeader* h, int32_t n, int hq, int gq,
                          void* o, float* lse, cudaStream_t stream) {
   const int64_t tasks = (int64_t)n * hq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tasks + kMergeWarps / W - 1) / (kMergeWarps / W)));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute beside = {};
-  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  beside.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &beside;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_q8_kernel<W>,
-                            reinterpret_cast<const float*>(base + h->off_part_o),
-                            reinterpret_cast<const float*>(base + h->off_part_lse),
-                            reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
-                            reinterpret_cast<const DecMergeRef*>(base + h->off_merge), (int)n, hq,
-                            gq, static_cast<__nv_bfloat16*>(o), lse);
+  return launch_beside(merge_q8_kernel<W>,
+                       dim3((unsigned)((tasks + kMergeWarps / W - 1) / (kMergeWarps / W))),
+                       dim3(32 * kMergeWarps), 0, stream,
+                       reinterpret_cast<const float*>(base + h->off_part_o),
+                       reinterpret_cast<const float*>(base + h->off_part_lse),
+                       reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
+                       reinterpret_cast<const DecMergeRef*>(base + h->off_merge), (int)n, hq, gq,
+                       static_cast<__nv_bfloat16*>(o), lse);
 }
 
 template <bool WIDE, int HBL>
@@ -639,17 +637,7 @@ cudaError_t launch_partials(const Params& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(1ull << dev);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute beside = {};
-  beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  beside.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &beside;
-  cfg.numAttrs = p.after_wide ? 1 : 0;  // what comes before a call's first kernel is not ours
-  return cudaLaunchKernelEx(&cfg, decode_q8_kernel<WIDE, HBL>, p);
+  return launch_beside(decode_q8_kernel<WIDE, HBL>, dim3(grid), dim3(kThreads), kSmem, stream, p);
 }
 
 }  // namespace

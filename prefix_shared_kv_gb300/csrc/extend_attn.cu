@@ -55,6 +55,7 @@
 
 #include <atomic>
 
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "rx_internal.h"
 #include "tc.cuh"
@@ -320,7 +321,7 @@ static __device__ __forceinline__ void producer_q8(const ExtParams& p, uint32_t 
   const int b_full = is_k ? B_K_FULL : B_V_FULL, b_free = is_k ? B_K_FREE : B_V_FREE;
   // the segments are written by the kernel before this one, which may still be running; what it
   // wrote is read by the copy engine
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_predecessors();
   asm volatile("fence.proxy.async;" ::: "memory");
   uint32_t gt = 0;
   bool ok = true;
@@ -1020,19 +1021,9 @@ int launch_items(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
     grid = n_items < n_sm ? n_items : n_sm;
   }
   if (grid <= 0) return 0;
-  if constexpr (Q8) {  // launched beside the kernel that expands the segments
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Tiles<Q8>::kSmem;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute beside = {};
-    beside.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    beside.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &beside;
-    cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, extend_tc_kernel<Q8>, p, k_map, v_map);
-  }
+  if constexpr (Q8)  // (beside the kernel that expands the segments)
+    return (int)launch_beside(extend_tc_kernel<Q8>, dim3(grid), dim3(kThreads), Tiles<Q8>::kSmem,
+                              (cudaStream_t)stream, p, k_map, v_map);
   extend_tc_kernel<Q8><<<grid, kThreads, Tiles<Q8>::kSmem, (cudaStream_t)stream>>>(p, k_map, v_map);
   return (int)cudaGetLastError();
 }

@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "rx_internal.h"
 
@@ -89,6 +90,8 @@ __global__ void __launch_bounds__(kThreads) store_q8_kernel(
   const int64_t st_tokens = stride / hkv;
   const int st_heads = (int)(stride - st_tokens * hkv);
   RowIter it((int64_t)blockIdx.x * (kThreads / 8) + threadIdx.x / 8, hkv);
+  wait_for_predecessors();
+  let_successors_start();
   // the eight lanes of a row leave together; a warp's four rows may not, hence the group's mask
   const uint32_t group = 0xffu << (threadIdx.x & 24);
   while (it.row < n_rows) {
@@ -167,6 +170,8 @@ __global__ void __launch_bounds__(kThreads) load_q8_kernel(
     }
   };
   int64_t first = it.row;
+  wait_for_predecessors();
+  let_successors_start();
   fetch();
   for (; first < n_rows; first += U * stride) {
     uint4 c[U];
@@ -227,11 +232,11 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     const int32_t* __restrict__ req_to_token, int64_t stride, int64_t pool_size, int hkv,
     float scale_log2, const Q8Tile* __restrict__ tiles, uint8_t* __restrict__ stage,
     int32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int32_t s_slot[kAttnKeys];
   __shared__ uint32_t s_nan[kExpandHeads];
   const Q8Tile tile = tiles[blockIdx.x];
   const int head0 = blockIdx.y * kExpandHeads, nh = min(kExpandHeads, hkv - head0);
+  wait_for_predecessors();
   if (threadIdx.x < kAttnKeys) {
     int s = -1;  // past the segment, or outside the pool (flagged): zeros
     if ((int)threadIdx.x < tile.n_keys) {
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
   }
   if (threadIdx.x < kExpandHeads) s_nan[threadIdx.x] = 0;
   __syncthreads();
+  let_successors_start();
   uint8_t* blocks = stage + ((int64_t)blockIdx.x * hkv + head0) * kQ8BlockBytes;
   for (int i = threadIdx.x; i < kAttnKeys * nh; i += kThreads) {
     const int key = i / nh, h = i - key * nh;
@@ -331,10 +337,10 @@ int launch_store_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const void* k_ne
   if (sms == 0) return (int)cudaGetLastError();
   const bool b32 = ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 31) == 0;
   auto run = [&](auto kernel, int u) {
-    kernel<<<rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), kThreads, 0, (cudaStream_t)stream>>>(
-        (uint8_t*)kv->k_code, (uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, (const uint4*)k_new,
-        (const uint4*)v_new, slots, rows, d->num_kv_heads, d->pool_size);
-    return (int)cudaGetLastError();
+    return (int)launch_beside(
+        kernel, rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), dim3(kThreads), 0,
+        (cudaStream_t)stream, (uint8_t*)kv->k_code, (uint8_t*)kv->v_code, kv->k_scale, kv->v_scale,
+        (const uint4*)k_new, (const uint4*)v_new, slots, rows, d->num_kv_heads, d->pool_size);
   };
   if (few_rows(rows, sms)) return b32 ? run(store_q8_kernel<1, true>, 1) : run(store_q8_kernel<1, false>, 1);
   return b32 ? run(store_q8_kernel<kManyRows, true>, kManyRows)
@@ -349,10 +355,10 @@ int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* sl
   if (sms == 0) return (int)cudaGetLastError();
   const bool b32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   auto run = [&](auto kernel, int u) {
-    kernel<<<rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), kThreads, 0, (cudaStream_t)stream>>>(
-        (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, slots,
-        (uint4*)k_out, (uint4*)v_out, rows, d->num_kv_heads, d->pool_size);
-    return (int)cudaGetLastError();
+    return (int)launch_beside(
+        kernel, rows_grid(rows, u, u == 1 ? rows : kManyCtas * sms), dim3(kThreads), 0,
+        (cudaStream_t)stream, (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale,
+        kv->v_scale, slots, (uint4*)k_out, (uint4*)v_out, rows, d->num_kv_heads, d->pool_size);
   };
   if (few_rows(rows, sms)) return b32 ? run(load_q8_kernel<1, true>, 1) : run(load_q8_kernel<1, false>, 1);
   return b32 ? run(load_q8_kernel<kManyRows, true>, kManyRows)
@@ -362,11 +368,11 @@ int launch_load_kv_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const int32_t* sl
 int launch_expand_q8(const rx_kv_desc* d, const rx_kv_q8* kv, const Q8Tile* tiles, int32_t n_tiles,
                      void* stage, int32_t* status, void* stream) {
   const dim3 grid(n_tiles, (d->num_kv_heads + kExpandHeads - 1) / kExpandHeads);
-  expand_q8_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(
-      (const uint8_t*)kv->k_code, (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale,
-      d->req_to_token, d->req_to_token_stride, d->pool_size, d->num_kv_heads,
+  return (int)launch_beside(
+      expand_q8_kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, (const uint8_t*)kv->k_code,
+      (const uint8_t*)kv->v_code, kv->k_scale, kv->v_scale, d->req_to_token,
+      d->req_to_token_stride, d->pool_size, d->num_kv_heads,
       d->softmax_scale * 1.4426950408889634f, tiles, (uint8_t*)stage, status);
-  return (int)cudaGetLastError();
 }
 
 }  // namespace rx

@@ -227,51 +227,66 @@ def kv_q8(k_code, v_code, k_scale, v_scale) -> KVQ8:
     return kv
 
 
-def _check_q8(desc: KVDesc, kv: KVQ8, named):
-    """An 8-bit call's tensors against the descriptor: the pool's shape and device, and per (name,
-    tensor, elements, dtype) size, dtype, layout and device.  Raw addresses (ints) and hand-made
-    KVQ8 structures are the caller's responsibility."""
+def _fits(t, n: int, dtype, device: int) -> bool:
+    """Whether a tensor has n contiguous elements of dtype on the device; raw addresses (ints) are
+    the caller's responsibility."""
+    try:
+        return (t.numel() == n and t.dtype is dtype and t.get_device() == device
+                and t.is_contiguous())
+    except AttributeError:
+        return t is None or type(t) is int
+
+
+def _call_q8(fn, desc: KVDesc, kv: KVQ8, named, args, stream):
+    """fn(*args, stream) after checking an 8-bit call's tensors: the pool's shape against the
+    descriptor, (name, tensor, elements, dtype) each, and that all are on the current device.  For a
+    hand-made KVQ8 the pool's shape and device are the caller's responsibility."""
     import torch
-    pool = getattr(kv, "shape", None)
-    if pool is not None and pool != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
-        raise ValueError(f"the pool is {pool}, the descriptor's "
-                         f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
-    where = kv.device if pool is not None else None
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() or _has_cuda() else -1
+    shape = getattr(kv, "shape", None)
+    if shape is not None:
+        if shape != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
+            raise ValueError(f"the pool is {shape}, the descriptor's "
+                             f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
+        if kv.device != device or device < 0:
+            raise ValueError(f"the pool is on device {kv.device}, the current CUDA device is "
+                             f"{device}")
     for name, t, n, dtype in named:
-        if type(t) is int or t is None:
-            continue
-        if t.numel() != n:
-            raise ValueError(f"{name} holds {t.numel()} elements; {n} expected")
-        if t.dtype is not dtype or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous {dtype} expected, got {t.dtype}")
-        if where is None:
-            where = t.get_device()
-        if t.get_device() != where or where < 0:
-            raise ValueError(f"{name} is on {t.device}, the pool on device {where}")
-    if where is not None and (where < 0 or where != torch.cuda.current_device()):
-        raise ValueError("the tensors are not on the current CUDA device")
+        if not _fits(t, n, dtype, device):
+            raise ValueError(f"{name}: {n} contiguous elements of {dtype} on CUDA device {device} "
+                             f"expected, got {t.numel()} of {t.dtype} on {t.device}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
+            else _stream(stream))
+    if st != RX_OK:
+        _check(st)
+
+
+def _has_cuda() -> bool:
+    import torch
+    return torch.cuda.is_available()
 
 
 def store_kv_q8(desc: KVDesc, kv: KVQ8, k_new, v_new, slots, stream=None):
     """rx_store_kv_q8: quantise bf16 rows k_new, v_new [n, Hkv, 128] into slots [n] of the pool."""
     import torch
-    n = int(slots.shape[0]) if slots is not None else 0
+    n = slots.shape[0] if slots is not None else 0
     row = n * desc.num_kv_heads * desc.head_dim
-    _check_q8(desc, kv, [("k_new", k_new, row, torch.bfloat16),
-                         ("v_new", v_new, row, torch.bfloat16), ("slots", slots, n, torch.int32)])
-    _check(lib().rx_store_kv_q8(C.byref(desc), C.byref(kv), _ptr(k_new), _ptr(v_new), _ptr(slots),
-                                n, _stream(stream)))
+    _call_q8(lib().rx_store_kv_q8, desc, kv,
+             (("k_new", k_new, row, torch.bfloat16), ("v_new", v_new, row, torch.bfloat16),
+              ("slots", slots, n, torch.int32)),
+             (C.byref(desc), C.byref(kv), _ptr(k_new), _ptr(v_new), _ptr(slots), n), stream)
 
 
 def load_kv_q8(desc: KVDesc, kv: KVQ8, slots, k_out, v_out, stream=None):
     """rx_load_kv_q8: read slots [n] of the pool back into bf16 rows k_out, v_out [n, Hkv, 128]."""
     import torch
-    n = int(slots.shape[0]) if slots is not None else 0
+    n = slots.shape[0] if slots is not None else 0
     row = n * desc.num_kv_heads * desc.head_dim
-    _check_q8(desc, kv, [("k_out", k_out, row, torch.bfloat16),
-                         ("v_out", v_out, row, torch.bfloat16), ("slots", slots, n, torch.int32)])
-    _check(lib().rx_load_kv_q8(C.byref(desc), C.byref(kv), _ptr(slots), n, _ptr(k_out),
-                               _ptr(v_out), _stream(stream)))
+    _call_q8(lib().rx_load_kv_q8, desc, kv,
+             (("k_out", k_out, row, torch.bfloat16), ("v_out", v_out, row, torch.bfloat16),
+              ("slots", slots, n, torch.int32)),
+             (C.byref(desc), C.byref(kv), _ptr(slots), n, _ptr(k_out), _ptr(v_out)), stream)
 
 
 class Plan:
@@ -410,19 +425,16 @@ def decode_attn(plan: Plan, desc: KVDesc, k_pool, v_pool, q, o, lse, workspace, 
                                 _stream(stream)))
 
 
-def _numel(t) -> int:
-    return t.numel() if hasattr(t, "numel") else 0
-
-
-def _attn_q8(call, plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream):
+def _attn_q8(fn, plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream):
     import torch
     n = plan.rows() * desc.num_q_heads
-    _check_q8(desc, kv, [("q", q, n * desc.head_dim, torch.bfloat16),
-                         ("o", o, n * desc.head_dim, torch.bfloat16),
-                         ("lse", lse, n, torch.float32),
-                         ("workspace", workspace, _numel(workspace), torch.uint8)])
-    _check(call(plan.handle, C.byref(desc), C.byref(kv), _ptr(q), _ptr(o), _ptr(lse),
-                _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    nd = n * desc.head_dim
+    ws = workspace.numel() if hasattr(workspace, "numel") else 0
+    _call_q8(fn, desc, kv,
+             (("q", q, nd, torch.bfloat16), ("o", o, nd, torch.bfloat16),
+              ("lse", lse, n, torch.float32), ("workspace", workspace, ws, torch.uint8)),
+             (plan.handle, C.byref(desc), C.byref(kv), _ptr(q), _ptr(o), _ptr(lse),
+              _ptr(workspace), ws), stream)
 
 
 def extend_attn_q8(plan: Plan, desc: KVDesc, kv: KVQ8, q, o, lse, workspace, stream=None):
