@@ -2,10 +2,13 @@
 //
 // With codes kc, vc (e4m3) and scales ks, vs (fp32) of key j, and base-2 scores
 //   s_j = scale log2(e) ks_j (q . kc_j):     o = sum_j 2^s_j vs_j vc_j / sum_j 2^s_j.
-// The codes are exact in fp16, so both products run on the fp16 tensor cores with fp32 sums: a warp's
-// query rows are brought to fp16 by a power of two that puts their largest magnitude in
-// [2^14, 2^15) (what the conversion loses is below 2^-39 of that magnitude, and the power comes back
-// in fp32).  With p_j = 2^(s_j - m), m a running reference of the row, the sum takes p_j and the
+// The codes are exact in fp16, so both products run on the fp16 tensor cores with fp32 sums.  A
+// warp's query rows are brought to fp16 by a common power of two, taken back in fp32, which puts
+// their largest magnitude H in [2^14, 2^15): what the conversion loses of an element is below
+// 2^-39 H, less than the fp32 sums of the row of H lose.  Rows of 2^20 or more, beside which that would
+// tell on another request's scores, have no part in it (unless all are that large, and within
+// 2^16): a warp computes them in fp32 by themselves when it is done with the others.
+// With p_j = 2^(s_j - m), m a running reference of the row, the sum takes p_j and the
 // second product's weights are p_j vs_j c, c a power of two of the row that keeps them at 2^8 or
 // less whatever the scales are: fp16 holds them to 2^-11 of their value down to 2^-14, and to
 // 2^-25 below.  m and c only move (and O is only rescaled) when some p_j or weight of the warp's
@@ -195,6 +198,111 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// The queries of a consumer warp in an item, and their power of two.
+template <int NT, bool WIDE, int HBL>
+struct Queries {
+  using F = Form<WIDE, HBL>;
+  const Params& p;
+  const DecItem& it;
+  int kw, row0, head, rows;  // the warp's 32-key run of a stage, first row, KV head; the item's rows
+  __device__ Queries(const Params& p_, const DecItem& it_) : p(p_), it(it_) {
+    const int warp = threadIdx.x >> 5;
+    kw = warp % (kWarps / F::kRowWarps);
+    row0 = warp / (kWarps / F::kRowWarps) * (8 * NT);
+    head = it.head_block * F::HB + (kw & (F::HB - 1));
+    rows = it.n_tok * p.gq;
+  }
+  // This lane's part of row row0 + 8 n + lane / 4: d = 16 k + 4 (lane % 4) .. + 3 for k = 0 .. 7.
+  __device__ void load(int n, uint2 (&x)[8]) const {
+    const int r = row0 + 8 * n + ((threadIdx.x & 31) >> 2);
+    const __nv_bfloat16* src =
+        p.q + ((int64_t)(r < rows ? __ldg(p.rows + it.row_begin + r / p.gq) : 0) * p.hq +
+               head * p.gq + r % p.gq) * kHeadDim + 4 * (threadIdx.x & 3);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      x[k] = r < rows ? __ldg(reinterpret_cast<const uint2*>(src + 16 * k)) : make_uint2(0, 0);
+  }
+  // Biased exponent of the row's largest magnitude (255: not finite; of a row below 2^-87, 40).
+  static __device__ int exponent(const uint2 (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      m = __vmaxu2(m, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return max((int)(max(m & 0xffffu, m >> 16) >> 7), 40);
+  }
+};
+
+// The partial result of one query row over the warp's keys of an item, in fp32, without the ring: a
+// lane takes a key's score, then four of the 128 columns.
+template <bool WIDE, int HBL>
+__device__ void run_far_row(const Params& p, const DecItem& it, int head, int split, int rows,
+                            int r) {
+  using F = Form<WIDE, HBL>;
+  const int lane = threadIdx.x & 31;
+  const int nkeys = it.k_end - it.k_begin;
+  const int32_t* table = p.req_to_token + (int64_t)it.kv_row * p.stride + it.k_begin;
+  const uint4* q = reinterpret_cast<const uint4*>(
+      p.q + ((int64_t)__ldg(p.rows + it.row_begin + r / p.gq) * p.hq + head * p.gq + r % p.gq) *
+                kHeadDim);
+  float m = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = split * kQ8WarpKeys; k0 < nkeys; k0 += F::NK) {
+    const bool live = k0 + lane < nkeys;
+    int slot = live ? __ldg(table + k0 + lane) : -1;
+    if (slot >= p.pool_size) slot = -1;  // (flagged by the producer; zeros)
+    const int64_t row = (int64_t)slot * p.hkv + head;
+    float s = 0.f, vs = 0.f;
+    if (slot >= 0) {
+      vs = __ldg(p.v_scale + row);
+#pragma unroll 1
+      for (int c = 0; c < 16; ++c) {
+        const uint2 k = __ldg(reinterpret_cast<const uint2*>(p.k_code + row * kHeadDim) + c);
+        const uint4 x = __ldg(q + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = e4m3x2_to_f32((i < 2 ? k.x : k.y) >> (16 * (i & 1)));
+          s += f.x * __uint_as_float(xs[i] << 16) + f.y * __uint_as_float(xs[i] & 0xffff0000u);
+        }
+      }
+      s *= __ldg(p.k_scale + row) * p.scale_log2;
+    }
+    if (!live) s = -CUDART_INF_F;
+    float x = s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+    const float m_new = fmaxf(m, x), ref = m_new == -CUDART_INF_F ? 0.f : m_new;
+    const float a = fast_exp2(m - ref), e = fast_exp2(s - ref), w = e * vs;
+    m = m_new;
+    l = l * a + e;  // this lane's keys
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= a;
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const int sj = __shfl_sync(0xffffffffu, slot, j);
+      if (sj < 0) continue;
+      const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(
+                                   p.v_code + ((int64_t)sj * p.hkv + head) * kHeadDim) + lane);
+      const float2 f0 = e4m3x2_to_f32(v), f1 = e4m3x2_to_f32(v >> 16);
+      o[0] += wj * f0.x;
+      o[1] += wj * f0.y;
+      o[2] += wj * f1.x;
+      o[3] += wj * f1.y;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  const int64_t prow = (int64_t)it.part + ((int64_t)split * p.hkv + head) * rows + r;
+  *reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 4 * lane) =
+      make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+  if (lane == 0)
+    p.part_lse[prow] =
+        l == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) + __log2f(l);
+}
+
 // One item on a consumer warp: NT tiles of 8 query rows.  Returns false when a wait gave up.
 template <int NT, bool WIDE, int HBL>
 __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uint32_t base,
@@ -216,42 +324,61 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
   // form keeps them in shared memory, written and read by the same lane.
   uint2 qf[WIDE ? 1 : 8][WIDE ? 1 : NT];
   uint2* sq = reinterpret_cast<uint2*>(smem + F::kOffQ + warp * F::kQWarp) + lane;
-  float qs;  // scale_log2 and the power of two
+  float qs;          // scale_log2 and the power of two
+  uint32_t far = 0;  // rows computed apart
   {
-    uint32_t m = 0;
-    auto row_ptr = [&](int n) {
-      const int r = row0 + 8 * n + g;
-      return r < rows ? reinterpret_cast<const uint2*>(
-                            p.q + ((int64_t)__ldg(p.rows + it.row_begin + r / p.gq) * p.hq +
-                                   head * p.gq + r % p.gq) * kHeadDim + 4 * c)
-                      : nullptr;
-    };
     uint2 x[WIDE ? 1 : NT][8];
-    auto load = [&](const uint2* src, uint2 (&y)[8]) {
+    int ex[NT];  // biased exponent of the row's largest magnitude (255: not finite)
+    auto load = [&](int n, uint2 (&y)[8]) {
+      const int r = row0 + 8 * n + g;
+      const __nv_bfloat16* src =
+          p.q + ((int64_t)(r < rows ? __ldg(p.rows + it.row_begin + r / p.gq) : 0) * p.hq +
+                 head * p.gq + r % p.gq) * kHeadDim + 4 * c;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        y[k] = src ? __ldg(src + 4 * k) : make_uint2(0, 0);
-        m = __vmaxu2(m, __vmaxu2(y[k].x & 0x7fff7fffu, y[k].y & 0x7fff7fffu));
-      }
+      for (int k = 0; k < 8; ++k)
+        y[k] = r < rows ? __ldg(reinterpret_cast<const uint2*>(src + 16 * k)) : make_uint2(0, 0);
     };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) load(row_ptr(n), x[WIDE ? 0 : n]);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
-    // biased exponent of the largest magnitude; rows below 2^-87 keep 2^-87's power
-    const int e = max((int)(max(m & 0xffffu, m >> 16) >> 7), 40);
-    const float up = __uint_as_float((uint32_t)(268 - e) << 23);
-    qs = __uint_as_float((uint32_t)(e - 14) << 23) * p.scale_log2;
+    int hi = 0, lo = 255;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if constexpr (WIDE) load(row_ptr(n), x[0]);  // (again, from the cache: fewer registers)
+      uint2(&y)[8] = x[WIDE ? 0 : n];
+      load(n, y);
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        m = __vmaxu2(m, __vmaxu2(y[k].x & 0x7fff7fffu, y[k].y & 0x7fff7fffu));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      ex[n] = (int)(max(m & 0xffffu, m >> 16) >> 7);
+      if (row0 + 8 * n + g < rows) {
+        lo = min(lo, ex[n]);
+        if (ex[n] < 127 + 20) hi = max(hi, ex[n]);
+      }
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (hi == 0) {  // zeros and subnormals, or large rows only
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = min(lo + 16, 254);
+    }
+    hi = max(hi, 40);
+    const float up = __uint_as_float((uint32_t)(268 - hi) << 23);
+    qs = __uint_as_float((uint32_t)(hi - 14) << 23) * p.scale_log2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // (a row that is not finite stays: its scores are NaN in its own column)
+      const bool apart = ex[n] > hi && ex[n] < 255;
+      const uint32_t some = __ballot_sync(0xffffffffu, apart && c == 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) far |= (some >> (4 * i) & 1u) << (8 * n + i);
+      uint2(&v)[8] = x[WIDE ? 0 : n];
+      if constexpr (WIDE) load(n, v);  // (again, from the cache: fewer registers)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint2 v = x[WIDE ? 0 : n][k];
-        const uint2 y = make_uint2(pack_f16(__uint_as_float(v.x << 16) * up,
-                                            __uint_as_float(v.x & 0xffff0000u) * up),
-                                   pack_f16(__uint_as_float(v.y << 16) * up,
-                                            __uint_as_float(v.y & 0xffff0000u) * up));
+        uint2 y = make_uint2(pack_f16(__uint_as_float(v[k].x << 16) * up,
+                                      __uint_as_float(v[k].x & 0xffff0000u) * up),
+                             pack_f16(__uint_as_float(v[k].y << 16) * up,
+                                      __uint_as_float(v[k].y & 0xffff0000u) * up));
+        if (apart) y = make_uint2(0, 0);
         if constexpr (WIDE)
           sq[(k * NT + n) * 32] = y;
         else
@@ -336,11 +463,10 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
       auto weigh = [&]() {  // weights and sums under the present references; the largest
         float top = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) add[n] = 0ull;
+        for (int n = 0; n < NT; ++n) {
+          add[n] = 0ull;
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float e0, e1, w0, w1;
@@ -355,6 +481,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
               top = fmax3(top, w0, w1);
               pt[t][n][h] = pack_f16(w0, w1);
             }
+        }
         return top;
       };
       if (__any_sync(0xffffffffu, weigh() > 256.f)) {
@@ -368,7 +495,8 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
           for (int j = 0; j < 2; ++j) {
             const float m_old = -m[j];
             const int ew = (int)(__float_as_uint(w[j]) >> 23) - 127;  // log2 c
-            float x1 = m_old, x2 = w[j] == 0.f ? kUnset : m_old - (float)ew;
+            const float m2_old = w[j] == 0.f ? kUnset : m_old - (float)ew;
+            float x1 = m_old, x2 = m2_old;
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -382,6 +510,8 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
               x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
               x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, off));
             }
+            // a column moves when it has to itself: another request's scores are no reason
+            if (!(x1 > m_old + 8.f || x2 > m2_old + 8.f)) continue;
             // c = 2^en with weights of at most about 1; none while every V scale was 0
             const int en = x2 == kUnset ? -127 : (int)rintf(fminf(fmaxf(x1 - x2, -126.f), 126.f));
             ls[j] *= fast_exp2(m_old - x1);
@@ -445,7 +575,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) ls[j] += __shfl_xor_sync(0xffffffffu, ls[j], off);
       const int r = row0 + 8 * n + 2 * c + j;
-      if (r >= rows) continue;
+      if (r >= rows || (far >> (8 * n + 2 * c + j) & 1u)) continue;
       const bool none = ls[j] == 0.f;
       const float f = none || w[j] == 0.f ? 0.f : 1.f / w[j] / ls[j];
       const int64_t row = (int64_t)it.part + ((int64_t)split * p.hkv + head) * rows + r;
@@ -456,6 +586,8 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
       if (g == 0) p.part_lse[row] = none ? -CUDART_INF_F : -m[j] + __log2f(ls[j]);
     }
   }
+  for (; far; far &= far - 1)  // (the warp's lanes hold the same rows)
+    run_far_row<WIDE, HBL>(p, it, head, split, rows, row0 + __ffs(far) - 1);
   return true;
 }
 

@@ -582,9 +582,9 @@ rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
           sum += c * (hkv / hb_of(u.kind));
         }
       }
-      std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
       int64_t longest = sum / sms;
-      if (costs.size() <= (size_t)16 * sms) {
+      if (costs.size() <= (size_t)16 * sms) {  // (more items even out by themselves)
+        std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
         std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
         for (int k = 0; k < sms; ++k) ends.push(0);
         for (int64_t c : costs) {

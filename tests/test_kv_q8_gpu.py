@@ -303,6 +303,40 @@ def test_decode_queries_of_every_size(cuda):
     check_decode(pool, q, o, lse, lens)
 
 
+@pytest.mark.parametrize("members", [3, 14])
+def test_decode_a_request_does_not_disturb_those_it_shares_a_prefix_with(cuda, members):
+    """Garbage in one request's query (a padded row: huge, infinite, NaN) leaves the results of the
+    others of its group as they were, bit for bit."""
+    rng = np.random.default_rng(50 + members)
+    lens = [150 + 3 * b for b in range(members)]
+    pool = Pool(cuda, rng, 8, 2, sum(lens) + 300,
+                random_table(rng, sum(lens) + 300, lens, {0: (list(range(members)), 140)}))
+    q, o, lse, _, _ = run_decode(pool, rng, lens, [0] * members, [140])
+    check_decode(pool, q, o, lse, lens)
+    for bad in (W.bf16_bits(np.full(1, 1e30))[0], 0x7F80, 0x7FC1, 0x0001):
+        q2 = q.copy()
+        q2[1] = bad
+        _, o2, lse2, _, _ = run_decode(pool, rng, lens, [0] * members, [140], q=q2)
+        rest = [b for b in range(members) if b != 1]
+        assert torch.equal(o2[rest], o[rest]) and torch.equal(lse2[rest], lse[rest])
+
+
+@pytest.mark.parametrize("members,large", [(3, [1]), (3, [0, 1, 2]), (14, [2, 13]), (1, [0])])
+def test_decode_queries_of_2_to_the_22_beside_ordinary_ones(cuda, members, large):
+    """Keys so small that queries of 2^22 have ordinary scores: they are as exact as any."""
+    rng = np.random.default_rng(70 + members + len(large))
+    lens = [150 + 30 * b for b in range(members)]
+    pool = Pool(cuda, rng, 8, 2, sum(lens) + 300,
+                random_table(rng, sum(lens) + 300, lens, {0: (list(range(members)), 140)}))
+    pool.ks *= np.float32(2.0 ** -22)
+    pool.upload()
+    x = rng.standard_normal((members, 8, 128))
+    x[large] *= 2.0 ** 22
+    x[large, 3] *= 8
+    q, o, lse, _, _ = run_decode(pool, rng, lens, [0] * members, [140], q=W.bf16_bits(x))
+    check_decode(pool, q, o, lse, lens)
+
+
 def test_decode_nan_rows_reach_their_readers_only(cuda):
     rng = np.random.default_rng(10)
     lens = [100, 100, 100, 260]
