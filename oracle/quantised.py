@@ -72,3 +72,27 @@ def attend_rows(q, keys, vals, vscale, visible, scale):
     p = np.exp(s - np.where(np.isfinite(lse), lse, 0.0)[:, None])
     sabs = np.where(visible, scale * (np.abs(q) @ np.abs(keys).T), 0.0).max(axis=1, initial=0.0)
     return o, lse, p @ np.abs(vals), sabs, (p * vscale[None, :]).max(axis=1, initial=0.0)
+
+
+def extend(q, k, v, req_to_token, req_idx, prefix_len, extend_len, cu_q, scale):
+    """As attention.extend over float64 pools k, v [P, Hkv, 128] (see `values`)."""
+    n_rows, hq, d = q.shape
+    gq = hq // k.shape[1]
+    o, lse = np.full((n_rows, hq, d), np.nan), np.full((n_rows, hq), np.nan)
+    for r in range(len(req_idx)):
+        p, e = int(prefix_len[r]), int(extend_len[r])
+        at = np.asarray(req_to_token[req_idx[r], :p + e], np.int64)
+        rows = slice(int(cu_q[r]), int(cu_q[r]) + e)
+        visible = np.arange(p + e)[None, :] <= (p + np.arange(e))[:, None]
+        x = A.bf16_to_f64(q[rows])
+        for h in range(hq):
+            o[rows, h], lse[rows, h] = A.attend(x[:, h], k[at, h // gq], v[at, h // gq], visible,
+                                                scale)
+    return o, lse
+
+
+def decode(q, k, v, req_to_token, req_idx, seq_len, scale):
+    """As attention.decode over float64 pools k, v [P, Hkv, 128]."""
+    n = len(req_idx)
+    return extend(q, k, v, req_to_token, req_idx, np.asarray(seq_len) - 1, np.ones(n, np.int64),
+                  np.arange(n + 1), scale)

@@ -2,7 +2,8 @@
 
 Holds the device tensors of a seeded workload (pools, request->slot table, per-step new KV, query
 rows, outputs, plans and workspaces) and runs its steps: rx_store_kv, then rx_extend_attn and/or
-rx_decode_attn.  Torch provides the device memory and the stream; every step of the path runs in
+rx_decode_attn, or the same over an 8-bit pool (rx_store_kv_q8, rx_extend_attn_q8,
+rx_decode_attn_q8).  Torch provides the device memory and the stream; every step of the path runs in
 librx's kernels.
 """
 from __future__ import annotations
@@ -67,15 +68,29 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
 
 
+def quantised_pool(desc, k_pool: torch.Tensor, v_pool: torch.Tensor, stream=None) -> rx.KVQ8:
+    """An 8-bit pool holding the rows of bf16 pools [pool_size, Hkv, 128], slot for slot."""
+    codes = [torch.empty(p.shape, dtype=torch.float8_e4m3fn, device=p.device)
+             for p in (k_pool, v_pool)]
+    scales = [torch.empty(p.shape[:2], dtype=torch.float32, device=p.device)
+              for p in (k_pool, v_pool)]
+    kv = rx.kv_q8(*codes, *scales)
+    slots = torch.arange(k_pool.shape[0], dtype=torch.int32, device=k_pool.device)
+    rx.store_kv_q8(desc, kv, k_pool, v_pool, slots, stream)
+    return kv
+
+
 class DeviceWorkload:
     """`pool_seed`: for a workload built structure-only (values=False, no cached KV drawn on the
     host), the pools are allocated on the device and every slot is filled with N(0,1) bf16 values
     from this seed (K with pool_seed, V with pool_seed + 1).  Used where only timing matters;
     parity checks use host-drawn pools, which the oracle reads too.  `extend_kernel`: the
-    tensor-core kernel the extend plans run on (rx.RX_EXTEND_TILES or rx.RX_EXTEND_PAIR)."""
+    tensor-core kernel the extend plans run on (rx.RX_EXTEND_TILES or rx.RX_EXTEND_PAIR).
+    `kv_type`: the pool the steps use; with rx.RX_KV_E4M3 the cached KV is quantised into an 8-bit
+    pool (`kv`) first, and the bf16 pools are dropped."""
 
     def __init__(self, wl: Workload, device="cuda", stream=None, pool_seed=None,
-                 extend_kernel=rx.RX_EXTEND_TILES):
+                 extend_kernel=rx.RX_EXTEND_TILES, kv_type=rx.RX_KV_BF16):
         self.wl = wl
         self.device = torch.device(device)
         self.stream = stream
@@ -93,6 +108,10 @@ class DeviceWorkload:
         self.r2t = to_i32(wl.req_to_token, self.device)
         self.desc = rx.kv_desc(wl.num_q_heads, wl.num_kv_heads, wl.pool_size, self.r2t,
                                wl.softmax_scale)
+        self.kv = quantised_pool(self.desc, self.k_pool, self.v_pool, stream) \
+            if kv_type == rx.RX_KV_E4M3 else None
+        if self.kv is not None:
+            self.k_pool = self.v_pool = None
         self.steps: List[DevStep] = []
         hq, d = wl.num_q_heads, wl.head_dim
         for st in wl.steps:
@@ -102,6 +121,7 @@ class DeviceWorkload:
                 e = st.extend
                 ds.ext_plan = rx.Plan()
                 ds.ext_plan.set_extend_kernel(extend_kernel)
+                ds.ext_plan.set_kv_type(kv_type)
                 rx.extend_plan(ds.ext_plan, self.desc, e.req_idx, e.prefix_len, e.extend_len,
                                e.group_of_req, e.group_prefix_len, e.group_parent)
                 ds.ext_ws = workspace(ds.ext_plan.workspace_size(), self.device)
@@ -113,6 +133,7 @@ class DeviceWorkload:
             if st.decode is not None:
                 dc = st.decode
                 ds.dec_plan = rx.Plan()
+                ds.dec_plan.set_kv_type(kv_type)
                 rx.decode_plan(ds.dec_plan, self.desc, dc.req_idx, dc.seq_len, dc.group_of_req,
                                dc.group_prefix_len, dc.group_parent)
                 ds.dec_ws = workspace(ds.dec_plan.workspace_size(), self.device)
@@ -125,17 +146,26 @@ class DeviceWorkload:
 
     def store(self, i: int):
         ds = self.steps[i]
+        if self.kv is not None:
+            rx.store_kv_q8(self.desc, self.kv, ds.k_new, ds.v_new, ds.slots, self.stream)
+            return
         rx.store_kv(self.desc, self.k_pool, self.v_pool, ds.k_new, ds.v_new, ds.slots, self.stream)
 
     def extend(self, i: int):
         ds = self.steps[i]
-        if ds.ext_plan is not None:
+        if ds.ext_plan is not None and self.kv is not None:
+            rx.extend_attn_q8(ds.ext_plan, self.desc, self.kv, ds.ext_q, ds.ext_o, ds.ext_lse,
+                              ds.ext_ws, self.stream)
+        elif ds.ext_plan is not None:
             rx.extend_attn(ds.ext_plan, self.desc, self.k_pool, self.v_pool, ds.ext_q, ds.ext_o,
                            ds.ext_lse, ds.ext_ws, self.stream)
 
     def decode(self, i: int):
         ds = self.steps[i]
-        if ds.dec_plan is not None:
+        if ds.dec_plan is not None and self.kv is not None:
+            rx.decode_attn_q8(ds.dec_plan, self.desc, self.kv, ds.dec_q, ds.dec_o, ds.dec_lse,
+                              ds.dec_ws, self.stream)
+        elif ds.dec_plan is not None:
             rx.decode_attn(ds.dec_plan, self.desc, self.k_pool, self.v_pool, ds.dec_q, ds.dec_o,
                            ds.dec_lse, ds.dec_ws, self.stream)
 

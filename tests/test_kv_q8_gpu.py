@@ -16,7 +16,7 @@ import torch
 
 from oracle import attention as A, quantised as Q
 from prefix_shared_kv_gb300 import rx, workloads as W
-from prefix_shared_kv_gb300.session import bits_of, to_bf16, to_i32, workspace
+from prefix_shared_kv_gb300.session import DeviceWorkload, bits_of, to_bf16, to_i32, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -676,3 +676,43 @@ def test_a_served_batch_through_the_8_bit_pool(cuda):
     for got, want in zip(out, (K, V)):
         # one rounding to float32 and one to bf16
         assert (np.abs(A.bf16_to_f64(bits_of(got)) - want) <= 2.0 ** -8 * 1.001 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("name", ["tiny", "tree"])
+def test_a_workload_over_the_8_bit_pool(cuda, name):
+    """The repository's own driver, every step: the tiny workload (extend, then decodes), and a radix
+    tree's mixed batch."""
+    wl = W.tiny() if name == "tiny" else W.tree_workload(
+        41, 8, 8, depth=2, fanout=3, seg_lo=50, seg_hi=300, p_empty=0.0, n_decode=40, tail_hi=40,
+        n_extend=6, own_hi=30, ext_lo=1, ext_hi=100)
+    dw = DeviceWorkload(wl, cuda, kv_type=rx.RX_KV_E4M3)
+    kp, vp = wl.k_pool, wl.v_pool
+    for i, st in enumerate(wl.steps):
+        dw.run_step(i)
+        torch.cuda.synchronize()
+        kp, vp = A.store_kv(kp, vp, st.k_new, st.v_new, st.store_slots)
+        (kc, ks), (vc, vs) = Q.quantise(kp), Q.quantise(vp)
+        ds = dw.steps[i]
+        for got, want in zip(dw.kv.tensors, (kc, vc, ks, vs)):
+            np.testing.assert_array_equal(got.view(torch.uint8).cpu().numpy().reshape(-1),
+                                          want.view(np.uint8).reshape(-1))
+        K, V = Q.values(kc, ks), Q.values(vc, vs)
+        todo = []
+        if st.extend is not None:
+            e = st.extend
+            todo.append((ds.ext_o, ds.ext_lse, e.q, EXT_ERR, Q.extend(
+                e.q, K, V, wl.req_to_token, e.req_idx, e.prefix_len, e.extend_len, e.cu_q,
+                wl.softmax_scale)))
+        if st.decode is not None:
+            d = st.decode
+            todo.append((ds.dec_o, ds.dec_lse, d.q, DEC_ERR, Q.decode(
+                d.q, K, V, wl.req_to_token, d.req_idx, d.seq_len, wl.softmax_scale)))
+        for o, lse, q, err, (ro, rl) in todo:
+            # |weights| sum to 1, |v| <= max |V|, S <= scale |q| |k| (Cauchy)
+            big = np.abs(V).max()
+            S = wl.softmax_scale * np.linalg.norm(A.bf16_to_f64(q), axis=-1) \
+                * np.linalg.norm(K, axis=-1).max()
+            e_s = 2.0 ** -19 * (S + 1)
+            tol = 2.0 ** -8 * np.abs(ro) + ((err + 2 * e_s) * big)[..., None] + 2.0 ** -20 * big
+            assert (np.abs(A.bf16_to_f64(bits_of(o)) - ro) <= tol).all()
+            assert (np.abs(lse.double().cpu().numpy() - rl) <= e_s + 2.0 ** -22 * np.abs(rl)).all()
