@@ -27,7 +27,9 @@
  *  Heads    query head h reads KV head h / (num_q_heads / num_kv_heads).
  *  Shapes   head_dim must be 128; num_q_heads / num_kv_heads in {1, 2, 4, 8}.
  *  Streams  Device work is enqueued on `stream` (a cudaStream_t, NULL = legacy default stream)
- *           and is asynchronous; calls return RX_OK once it is enqueued.
+ *           and is asynchronous; calls return RX_OK once it is enqueued.  A plan's workspace serves
+ *           one call at a time: calls that may overlap (other streams, graphs replayed at the same
+ *           time) take workspaces of their own, each uploaded to.
  *  Errors   Argument checks run on the host before anything is enqueued; a failed check returns
  *           its code and enqueues nothing.  rx_last_error() gives a message for the calling
  *           thread's last failure.  Kernels never trap and never wait without a bound: a device
@@ -150,7 +152,9 @@ rx_status rx_plan_set_extend_kernel(rx_plan* plan, int32_t kernel);
 #define RX_KV_E4M3 1
 rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
- * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge).
+ * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge; over
+ * an 8-bit pool an extend launches two, expansion and attention, and a merge if its keys are split,
+ * a decode wide items, narrow items and merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
 rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches);
 /* Rows of q / o / lse an attention call with the built plan reads and writes: the sum of
@@ -205,7 +209,11 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
  * with fp32 sums of exact products of the codes.  Scales of keys a row does not see, NaN ones
- * included, do not reach it.  pool_size * num_kv_heads is not limited. */
+ * included, do not reach it.  pool_size * num_kv_heads is not limited.
+ * The call first expands each distinct key of the plan into its workspace, once for all the query
+ * tiles that read it: rx_plan_workspace_size is about 522 bytes per distinct key and KV head (each
+ * shared prefix and each request's own keys rounded up to 64).  A batch whose tiles would leave SMs
+ * idle (a few new tokens on a long prefix) has the tiles' keys split over the SMs and merged. */
 rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream);
@@ -273,7 +281,8 @@ rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
  * with fp32 sums of exact products of the codes.  A key whose K scale is NaN makes o and lse of
- * the requests that read it NaN, a NaN V scale their o. */
+ * the requests that read it NaN, a NaN V scale their o.  The shared prefix of up to 64 stacked query
+ * rows (requests x query heads per KV head) is read once; a larger group reads it once per 64. */
 rx_status rx_decode_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream);
