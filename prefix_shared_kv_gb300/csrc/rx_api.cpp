@@ -38,6 +38,17 @@ rx_status cuda_fail(int e, const char* what) {
   return fail(RX_ERR_CUDA, "%s: %s", what, cudaGetErrorString((cudaError_t)e));
 }
 
+// A planner's result; no C++ exception leaves a C entry (the plan may then be of no kind, or the one
+// it was).
+template <class F>
+rx_status no_throw(F&& plan) {
+  try {
+    return plan();
+  } catch (const std::exception& e) {
+    return fail(RX_ERR_WORKSPACE, "the plan does not fit the host's memory (%s)", e.what());
+  }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 rx_status check_desc(const rx_kv_desc* d, bool need_table) {
@@ -462,10 +473,25 @@ rx_status rx_decode_plan(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
                              group_prefix_len, nullptr);
 }
 
+static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
+                                  const int32_t* req_idx, const int32_t* seq_len,
+                                  const int32_t* group_of_req, int32_t num_groups,
+                                  const int32_t* group_prefix_len, const int32_t* group_parent);
+
 rx_status rx_decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
                               const int32_t* req_idx, const int32_t* seq_len,
                               const int32_t* group_of_req, int32_t num_groups,
                               const int32_t* group_prefix_len, const int32_t* group_parent) {
+  return no_throw([&] {
+    return decode_plan_tree(plan, desc, batch, req_idx, seq_len, group_of_req, num_groups,
+                            group_prefix_len, group_parent);
+  });
+}
+
+static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
+                                  const int32_t* req_idx, const int32_t* seq_len,
+                                  const int32_t* group_of_req, int32_t num_groups,
+                                  const int32_t* group_prefix_len, const int32_t* group_parent) {
   if (!plan) return fail(RX_ERR_INVALID, "plan is NULL");
   rx_status st = check_desc(desc, true);
   if (st) return st;
@@ -864,11 +890,28 @@ rx_status rx_extend_plan(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
                              num_groups, group_prefix_len, nullptr);
 }
 
+static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
+                                  const int32_t* req_idx, const int32_t* prefix_len,
+                                  const int32_t* extend_len, const int32_t* group_of_req,
+                                  int32_t num_groups, const int32_t* group_prefix_len,
+                                  const int32_t* group_parent);
+
 rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
                               const int32_t* req_idx, const int32_t* prefix_len,
                               const int32_t* extend_len, const int32_t* group_of_req,
                               int32_t num_groups, const int32_t* group_prefix_len,
                               const int32_t* group_parent) {
+  return no_throw([&] {
+    return extend_plan_tree(plan, desc, batch, req_idx, prefix_len, extend_len, group_of_req,
+                            num_groups, group_prefix_len, group_parent);
+  });
+}
+
+static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
+                                  const int32_t* req_idx, const int32_t* prefix_len,
+                                  const int32_t* extend_len, const int32_t* group_of_req,
+                                  int32_t num_groups, const int32_t* group_prefix_len,
+                                  const int32_t* group_parent) {
   if (!plan) return fail(RX_ERR_INVALID, "plan is NULL");
   rx_status st = check_desc(desc, true);
   if (st) return st;

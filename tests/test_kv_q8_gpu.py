@@ -716,3 +716,219 @@ def test_a_workload_over_the_8_bit_pool(cuda, name):
             tol = 2.0 ** -8 * np.abs(ro) + ((err + 2 * e_s) * big)[..., None] + 2.0 ** -20 * big
             assert (np.abs(A.bf16_to_f64(bits_of(o)) - ro) <= tol).all()
             assert (np.abs(lse.double().cpu().numpy() - rl) <= e_s + 2.0 ** -22 * np.abs(rl)).all()
+
+
+# ---- calls as the documentation allows them ----------------------------------------------------
+
+def test_tensors_at_16_byte_but_not_32_byte_addresses(cuda):
+    rng = np.random.default_rng(81)
+    hkv, T, P = 4, 700, 900
+
+    def odd(shape, dtype):  # a view that starts 16 bytes behind a 512-byte boundary
+        n = int(np.prod(shape))
+        size = torch.empty(0, dtype=dtype).element_size()
+        base = torch.zeros(n + 64, dtype=dtype, device=cuda)
+        view = base[16 // size:16 // size + n].view(shape)
+        assert view.data_ptr() % 32 == 16
+        return view
+
+    code = [odd((P, hkv, 128), torch.uint8) for _ in range(2)]
+    scale = [odd((P, hkv), torch.float32) for _ in range(2)]
+    kv = rx.kv_q8(*code, *scale)
+    new = [odd((T, hkv, 128), torch.bfloat16) for _ in range(2)]
+    out = [odd((T, hkv, 128), torch.bfloat16) for _ in range(2)]
+    bits = [W.normal_bf16(rng, (T, hkv, 128)) for _ in range(2)]
+    for n, b in zip(new, bits):
+        n.copy_(to_bf16(b, cuda))
+    slots = rng.permutation(P)[:T].astype(np.int32)
+    table = to_i32(np.array([slots]), cuda)
+    desc = rx.kv_desc(8, hkv, P, table)
+    rx.store_kv_q8(desc, kv, *new, to_i32(slots, cuda))
+    rx.load_kv_q8(desc, kv, to_i32(slots, cuda), *out)
+    want = [Q.quantise(b) for b in bits]
+    for i in range(2):
+        assert np.array_equal(code[i].cpu().numpy()[slots], want[i][0])
+        assert np.array_equal(scale[i].cpu().numpy()[slots], want[i][1])
+        x = torch.from_numpy(Q.VALUES[want[i][0]].astype(np.float32) * want[i][1][..., None])
+        assert torch.equal(out[i].cpu(), x.to(torch.bfloat16))
+    K, V = (Q.values(*w) for w in want)
+    for kind in ("decode", "extend"):
+        n = 1 if kind == "decode" else 50
+        q, o, lse = odd((n, 8, 128), torch.bfloat16), odd((n, 8, 128), torch.bfloat16), odd(
+            (n, 8), torch.float32)
+        qb = W.normal_bf16(rng, (n, 8, 128))
+        q.copy_(to_bf16(qb, cuda))
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        if kind == "decode":
+            rx.decode_plan(plan, desc, [0], [T])
+        else:
+            rx.extend_plan(plan, desc, [0], [T - n], [n])
+        ws = workspace(plan.workspace_size(), cuda)
+        plan.upload(ws)
+        (rx.decode_attn_q8 if kind == "decode" else rx.extend_attn_q8)(plan, desc, kv, q, o, lse, ws)
+        torch.cuda.synchronize()
+        at = np.arange(T)[None]
+        ro, rl = Q.extend(qb, K, V, at, [0], [T - n], [n], [0, n], 128 ** -0.5)
+        assert np.abs(A.bf16_to_f64(bits_of(o)) - ro).max() <= 2.0 ** -6 * np.abs(V).max()
+        assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3
+
+
+def test_nothing_is_written_outside_the_outputs(cuda):
+    """Guard bands around the outputs, the pool and the workspace of every call."""
+    rng = np.random.default_rng(82)
+    band = 4096
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        base = torch.full(((n + 2 * band) * torch.empty(0, dtype=dtype).element_size(),), 0xA5,
+                          dtype=torch.uint8, device=cuda).view(dtype)
+        return base, base[band:band + n].view(shape)
+
+    def untouched(base, n):
+        raw = base.view(torch.uint8).cpu().numpy()
+        b = band * base.element_size()
+        return (raw[:b] == 0xA5).all() and (raw[-b:] == 0xA5).all()
+
+    P, hkv, hq = 700, 3, 12
+    lens = [200, 333, 64]
+    table = random_table(rng, P, lens)
+    kept = [guarded((P, hkv, 128), torch.uint8) for _ in range(2)] + \
+        [guarded((P, hkv), torch.float32) for _ in range(2)]
+    kv = rx.kv_q8(*(t for _, t in kept))
+    r2t = to_i32(table, cuda)
+    desc = rx.kv_desc(hq, hkv, P, r2t)
+    slots = to_i32(rng.permutation(P).astype(np.int32), cuda)
+    new = [to_bf16(W.normal_bf16(rng, (P, hkv, 128)), cuda) for _ in range(2)]
+    rx.store_kv_q8(desc, kv, *new, slots)
+    out = [guarded((P, hkv, 128), torch.bfloat16) for _ in range(2)]
+    rx.load_kv_q8(desc, kv, slots, out[0][1], out[1][1])
+    kept += out
+    for kind in ("decode", "extend"):
+        n = 3 if kind == "decode" else 120
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        if kind == "decode":
+            rx.decode_plan(plan, desc, np.arange(3), lens)
+        else:
+            rx.extend_plan(plan, desc, np.arange(3), [l - 40 for l in lens], [40] * 3)
+        size = plan.workspace_size()
+        ws = guarded((size,), torch.uint8)
+        plan.upload(ws[1])
+        o, lse = guarded((n, hq, 128), torch.bfloat16), guarded((n, hq), torch.float32)
+        q = to_bf16(W.normal_bf16(rng, (n, hq, 128)), cuda)
+        (rx.decode_attn_q8 if kind == "decode" else rx.extend_attn_q8)(
+            plan, desc, kv, q, o[1], lse[1], ws[1])
+        torch.cuda.synchronize()
+        assert torch.isfinite(o[1].float()).all() and torch.isfinite(lse[1]).all()
+        kept += [ws, o, lse]
+    for base, t in kept:
+        assert untouched(base, t.numel())
+
+
+def test_extend_on_two_streams_and_in_a_captured_graph(cuda):
+    prefix, new = [300, 40], [200, 90]
+    rng, pool, _, _ = extend_case(cuda, 83, 16, 4, prefix, new)
+    q = [W.normal_bf16(rng, (290, 16, 128)) for _ in range(2)]
+    work = []
+    for i in range(2):
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        rx.extend_plan(plan, pool.desc, [0, 1], prefix, new)
+        ws = workspace(plan.workspace_size(), cuda)
+        plan.upload(ws)
+        work.append((plan, ws, to_bf16(q[i], cuda),
+                     torch.empty((290, 16, 128), dtype=torch.bfloat16, device=cuda),
+                     torch.empty((290, 16), device=cuda), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for plan, ws, dq, o, lse, s in work:
+            rx.extend_attn_q8(plan, pool.desc, pool.kv, dq, o, lse, ws, stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        check_extend(pool, q[i], work[i][3], work[i][4], prefix, new)
+    plan, ws, dq, o, lse, _ = work[0]
+    slots = np.concatenate([pool.table[r, prefix[r]:prefix[r] + new[r]] for r in range(2)])
+    rows = [W.normal_bf16(rng, (290, 4, 128)) for _ in range(4)]
+    dk, dv, ds = to_bf16(rows[0], cuda), to_bf16(rows[1], cuda), to_i32(slots, cuda)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rx.store_kv_q8(pool.desc, pool.kv, dk, dv, ds)
+        rx.extend_attn_q8(plan, pool.desc, pool.kv, dq, o, lse, ws)
+    for k, v in (rows[:2], rows[2:]):
+        dk.copy_(to_bf16(k, cuda))
+        dv.copy_(to_bf16(v, cuda))
+        o.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        pool.kc[slots], pool.ks[slots] = Q.quantise(k)
+        pool.vc[slots], pool.vs[slots] = Q.quantise(v)
+        check_extend(pool, q[0], o, lse, prefix, new)
+
+
+def test_one_plan_serves_every_layer(cuda):
+    """The same plan and workspace over several pools, one call right behind the other."""
+    rng = np.random.default_rng(84)
+    lens, prefix, new = [400, 70, 900], [300, 20, 850], [100, 50, 50]
+    pools = [Pool(cuda, rng, 8, 4, 1500, random_table(rng, 1500, lens)) for _ in range(3)]
+    for pl in pools[1:]:  # one table for all layers
+        pl.table, pl.r2t, pl.desc = pools[0].table, pools[0].r2t, pools[0].desc
+    for kind in ("decode", "extend"):
+        n = 3 if kind == "decode" else 200
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        if kind == "decode":
+            rx.decode_plan(plan, pools[0].desc, np.arange(3), lens)
+        else:
+            rx.extend_plan(plan, pools[0].desc, np.arange(3), prefix, new)
+        ws = workspace(plan.workspace_size(), cuda)
+        plan.upload(ws)
+        q = [W.normal_bf16(rng, (n, 8, 128)) for _ in pools]
+        dq = [to_bf16(x, cuda) for x in q]
+        res = [(torch.empty((n, 8, 128), dtype=torch.bfloat16, device=cuda),
+                torch.empty((n, 8), device=cuda)) for _ in pools]
+        torch.cuda.synchronize()
+        for pl, x, (o, lse) in zip(pools, dq, res):
+            (rx.decode_attn_q8 if kind == "decode" else rx.extend_attn_q8)(
+                plan, pl.desc, pl.kv, x, o, lse, ws)
+        torch.cuda.synchronize()
+        for pl, x, (o, lse) in zip(pools, q, res):
+            if kind == "decode":
+                check_decode(pl, x, o, lse, lens)
+            else:
+                check_extend(pl, x, o, lse, prefix, new)
+
+
+def test_other_softmax_scales_and_many_heads(cuda):
+    rng = np.random.default_rng(85)
+    lens = [130, 61, 4]
+    for hq, hkv, scale in ((8, 8, 0.3), (256, 256, 0.02), (144, 72, 128 ** -0.5)):
+        pool = Pool(cuda, rng, hq, hkv, 260, random_table(rng, 260, lens))
+        pool.scale = float(np.float32(scale))
+        pool.desc = rx.kv_desc(hq, hkv, 260, pool.r2t, scale)
+        q, o, lse, _, _ = run_decode(pool, rng, lens)
+        check_decode(pool, q, o, lse, lens)
+        q, o, lse, _ = run_extend(pool, rng, [100, 1, 0], [30, 60, 4])
+        check_extend(pool, q, o, lse, [100, 1, 0], [30, 60, 4])
+
+
+def test_a_batch_of_thousands_of_short_requests(cuda):
+    rng = np.random.default_rng(86)
+    lens = [int(x) for x in rng.integers(1, 40, 3000)]
+    n = sum(lens) + 10
+    pool = Pool(cuda, rng, 4, 2, n, random_table(rng, n, lens))
+    q, o, lse, ws, _ = run_decode(pool, rng, lens)
+    pick = [0, 1, 2, 1499, 2998, 2999] + [int(x) for x in rng.integers(0, 3000, 60)]
+    check_decode(pool, q, o, lse, lens, pick)
+    assert torch.isfinite(o.float()).all() and rx.read_status(ws) == rx.RX_OK
+
+
+def test_calls_without_a_workspace_refuse_an_8_bit_plan(cuda):
+    rng = np.random.default_rng(87)
+    pool = Pool(cuda, rng, 8, 2, 64, random_table(rng, 64, [8]))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.decode_plan(plan, pool.desc, [0], [8])
+    with pytest.raises(rx.RxError) as e:
+        rx.decode_attn_noalloc(plan, pool.desc, 4096, 4096, 4096, 4096, 4096)
+    assert e.value.status == rx.RX_ERR_INVALID and "8-bit pool" in str(e.value)
