@@ -154,7 +154,8 @@ rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
  * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge; over
  * an 8-bit pool an extend launches two, expansion and attention, and a merge if its keys are split,
- * a decode wide items, narrow items and merge).
+ * a decode up to five: expansion and attention of very large groups, wide items, narrow items,
+ * merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
 rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches);
 /* Rows of q / o / lse an attention call with the built plan reads and writes: the sum of
@@ -282,7 +283,8 @@ rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
  * with fp32 sums of exact products of the codes.  A key whose K scale is NaN makes o and lse of
  * the requests that read it NaN, a NaN V scale their o.  The shared prefix of up to 64 stacked query
- * rows (requests x query heads per KV head) is read once; a larger group reads it once per 64. */
+ * rows (requests x query heads per KV head) is read once, of up to 128 once per 64; that of a
+ * larger group is read once and expanded into the workspace (522 bytes per key and KV head). */
 rx_status rx_decode_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream);

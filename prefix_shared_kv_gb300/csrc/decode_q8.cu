@@ -32,6 +32,9 @@
 // 16,000 shared keys, whole call: 278 us; 16-key steps, which halve the independent products, 294
 // us; 224 or 216 registers for the consumers, with spills, 288 and 306 us; the references in shared
 // memory instead of spills, 284 us.)
+// (A shared prefix of more than 128 rows is not run here: its keys are expanded as for an
+// extend, which moves three times their bytes, and the tensor-core tile kernel takes 256 rows at a
+// time.)
 // A persistent CTA per SM runs the list of items that the planner gave it.  Each item leaves
 // normalised fp32 partial rows and base-2 log-sum-exps, which a last kernel merges.  The kernels are
 // chained by programmatic dependent launch: the narrow one starts as SMs come free of the wide
@@ -797,6 +800,17 @@ int launch_decode_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   cudaStream_t s = (cudaStream_t)stream;
   const int hbl = q8_head_block_log2(p.hkv);
   cudaError_t e = cudaSuccess;
+  if (h->n_xitems > 0) {  // shared prefixes of very many rows
+    uint8_t* stage = base + h->off_q8_stage;
+    int x = launch_expand_q8(d, kv, reinterpret_cast<const Q8Tile*>(base + h->off_q8_tiles),
+                             h->n_q8_tiles, stage, p.status, stream);
+    if (!x)
+      x = launch_tiles_q8(d, reinterpret_cast<const ExtItem*>(base + h->off_xitems),
+                          reinterpret_cast<const ExtRow*>(base + h->off_xrows),
+                          reinterpret_cast<const ExtSeg*>(base + h->off_xsegs), h->n_xitems, stage,
+                          q, p.part_o, p.part_lse, p.status, stream);
+    if (x) return x;
+  }
   if (h->n_wide > 0) {
     p.items = reinterpret_cast<const DecItem*>(base + h->off_wide);
     p.cta_begin = reinterpret_cast<const int32_t*>(base + h->off_wide_cta);

@@ -1055,6 +1055,13 @@ int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                            v_pool, q, o, lse, nullptr, nullptr, status, stream);
 }
 
+int launch_tiles_q8(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
+                    const ExtSeg* segs, int32_t n_items, const void* stage, const void* q,
+                    float* part_o, float* part_lse, int32_t* status, void* stream) {
+  return launch_items<true>(d, items, rows, segs, n_items, nullptr, 0, nullptr, nullptr, stage, q,
+                            nullptr, nullptr, part_o, part_lse, status, stream);
+}
+
 int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
                      void* o, float* lse, void* ws, void* stream) {
   if (h->n_items == 0) return 0;

@@ -386,7 +386,7 @@ rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches) {
   // when its tiles' keys are split)
   *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3) +
                                                    (h.n_part_rows > 0))
-                              : (h.n_xitems > 0) + (h.n_wide > 0) + (h.n_items > 0) + (h.batch > 0);
+                              : (h.n_xitems > 0) * (1 + (h.kv_type == RX_KV_E4M3)) + (h.n_wide > 0) + (h.n_items > 0) + (h.batch > 0);
   return RX_OK;
 }
 
@@ -560,7 +560,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
     if (!members[g].empty() && group_prefix_len[g] > node_lo(g)) {
       const int len = group_prefix_len[g] - node_lo(g);
       total += (double)len * hkv * key_bytes * ((members[g].size() + max_tok - 1) / max_tok);
-      for (size_t t0 = 0; q8 && t0 < members[g].size(); t0 += max_tok) {
+      const bool tiles = (int64_t)members[g].size() * gq >= kQ8TileRows;  // not items of these forms
+      for (size_t t0 = 0; q8 && !tiles && t0 < members[g].size(); t0 += max_tok) {
         const int r = (int)std::min<size_t>(max_tok, members[g].size() - t0) * gq;
         spans.push_back({kind_of_rows(r), r, len});
       }
@@ -654,12 +655,14 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   std::vector<ExtItem> xitems;
   std::vector<ExtRow> xrows;
   std::vector<ExtSeg> xsegs;
+  std::vector<Q8Tile> tiles8;  // 8-bit pool: the tiles of their keys, in the segments' order
   int64_t key_reads = 0;
   for (int g = 0; g < num_groups; ++g) {
     const int lo = node_lo(g), hi = group_prefix_len[g];
     const auto& mem = members[g];
     if (mem.empty() || hi <= lo) continue;
-    if (tc_ok && !q8 && (int64_t)mem.size() * gq >= 32) {
+    const int64_t tc_rows = (int64_t)mem.size() * gq;
+    if (q8 ? tc_rows >= kQ8TileRows : tc_ok && tc_rows >= 32) {
       struct XTile {
         int row_begin, n_tok, t0;
       };
@@ -675,7 +678,9 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       for (int c0 = lo; c0 < hi; c0 += clen) {
         const int c1 = std::min(hi, c0 + clen);
         const int seg = (int)xsegs.size();
-        xsegs.push_back({req_idx[mem[0]], c0, c1, -1});
+        xsegs.push_back({q8 ? (int32_t)tiles8.size() : req_idx[mem[0]], c0, c1, -1});
+        for (int k = c0; q8 && k < c1; k += kAttnKeys)
+          tiles8.push_back({req_idx[mem[0]], k, std::min(kAttnKeys, c1 - k), 0});
         std::vector<int64_t> part(tiles.size());
         for (size_t k = 0; k < tiles.size(); ++k) {
           part[k] = npart;
@@ -700,7 +705,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
             it.part[1] = pair ? (int32_t)(part[k + 1] + (int64_t)h * tiles[k + 1].n_tok * gq) : 0;
             xitems.push_back(it);
           }
-          key_reads += (int64_t)(c1 - c0) * hkv;
+          if (!q8 || k == 0) key_reads += (int64_t)(c1 - c0) * hkv;  // (expanded once)
         }
       }
       continue;
@@ -734,7 +739,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       refer(b, 0, part, c.second - c.first, gq, 0);
     }
   }
-  if (npart > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
+  if (npart > (int64_t)INT32_MAX || (int64_t)tiles8.size() * hkv > (int64_t)INT32_MAX)
+    return fail(RX_ERR_RANGE, "plan too large");
 
   std::vector<DecItem> items, wide;
   for (const Unit& u : units) {
@@ -819,6 +825,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   h.n_xitems = (int32_t)xitems.size();
   h.off_cta = off; off = align256(off + cta_begin.size() * sizeof(int32_t));
   h.n_ctas = cta_begin.empty() ? 0 : (int32_t)cta_begin.size() - 1;
+  h.off_q8_tiles = off; off = align256(off + tiles8.size() * sizeof(Q8Tile));
+  h.n_q8_tiles = (int32_t)tiles8.size();
   h.off_wide = off; off = align256(off + wide.size() * sizeof(DecItem));
   h.off_wide_cta = off; off = align256(off + wide_begin.size() * sizeof(int32_t));
   h.n_wide = (int32_t)wide.size();
@@ -828,6 +836,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
   h.off_part_lse = off; off = align256(off + (size_t)npart * 4);
   h.n_part_rows = npart;
+  h.off_q8_stage = off; off = align256(off + tiles8.size() * (size_t)hkv * kQ8BlockBytes);
   h.total_bytes = off;
   plan->blob.assign(tables, 0);
   std::memcpy(plan->blob.data(), &h, sizeof h);
@@ -839,6 +848,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   put(plan->blob, h.off_xrows, xrows);
   put(plan->blob, h.off_xsegs, xsegs);
   put(plan->blob, h.off_cta, cta_begin);
+  put(plan->blob, h.off_q8_tiles, tiles8);
   put(plan->blob, h.off_wide, wide);
   put(plan->blob, h.off_wide_cta, wide_begin);
   plan->ws_bytes = off;

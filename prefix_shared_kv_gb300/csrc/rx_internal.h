@@ -54,7 +54,11 @@ constexpr size_t kDecSmemBytes = (size_t)kDecStages * kDecStageBytes + kDecMaxKe
 // warps (narrow) or four pairs of warps (wide) take a head each, 32 keys a stage; with fewer heads
 // they split a stage's keys.  A work unit's partial rows: [split][KV head][row].
 constexpr int kQ8WarpKeys = 32;
-constexpr int kQ8MaxRows = 16, kQ8MaxWideRows = 64;
+// A shared prefix of kQ8TileRows stacked rows or more goes to the tensor-core tile kernel instead,
+// 256 rows at a time, its keys expanded first.  (8 groups on 8,000 tokens, 8 KV heads, wide items
+// against tiles: 96 rows 135 / 159 us, 128 rows 142 / 150, 160 rows 221 / 186, 192 rows 222 / 192;
+// 4 groups of 256 rows 140 / 93, 2 of 512 139 / 78.)
+constexpr int kQ8MaxRows = 16, kQ8MaxWideRows = 64, kQ8TileRows = 129;
 inline int q8_head_block_log2(int hkv) {
   return hkv % 8 == 0 ? 3 : hkv % 4 == 0 ? 2 : hkv % 2 == 0 ? 1 : 0;
 }
@@ -174,6 +178,10 @@ int launch_decode(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
 int launch_extend(const rx_kv_desc* d, const PlanHeader* h, const void* k_pool,
                   const void* v_pool, const void* q, void* o, float* lse, void* ws,
                   void* stream);
+// The tile kernel over expanded blocks, partial rows out (decode plans).
+int launch_tiles_q8(const rx_kv_desc* d, const ExtItem* items, const ExtRow* rows,
+                    const ExtSeg* segs, int32_t n_items, const void* stage, const void* q,
+                    float* part_o, float* part_lse, int32_t* status, void* stream);
 int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* kv, const void* q,
                      void* o, float* lse, void* ws, void* stream);
 // The merge of a plan's partial rows (merge tables and partials of `ws`) into rows 0 .. n - 1 of o and

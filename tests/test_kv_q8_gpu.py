@@ -172,6 +172,7 @@ def test_load_is_the_definition_bit_for_bit(cuda, hkv, T):
 # ---- decode -----------------------------------------------------------------------------------
 
 DEC_ERR = 2.0 ** -11  # fp16 weights
+EXT_ERR = 2.0 ** -8 + 2.0 ** -24  # bf16 weights, the V scale's product
 
 
 def run_decode(pool, rng, lens, group_of_req=None, group_prefix_len=None, group_parent=None,
@@ -193,10 +194,10 @@ def run_decode(pool, rng, lens, group_of_req=None, group_prefix_len=None, group_
     return q, o, lse, ws, plan
 
 
-def check_decode(pool, q, o, lse, lens, pick=None):
+def check_decode(pool, q, o, lse, lens, pick=None, err=DEC_ERR):
     for b in (range(len(lens)) if pick is None else pick):
         pool.check(o[b:b + 1], lse[b:b + 1], q[b:b + 1], b, lens[b],
-                   np.ones((1, lens[b]), bool), DEC_ERR, f"request {b} of {lens[b]} keys")
+                   np.ones((1, lens[b]), bool), err, f"request {b} of {lens[b]} keys")
 
 
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (4, 4), (8, 1), (1, 1), (6, 3), (40, 5), (12, 12),
@@ -213,7 +214,8 @@ def test_decode_own_keys(cuda, hq, hkv):
 
 @pytest.mark.parametrize("hq,hkv,members", [(8, 2, 4), (8, 8, 3), (8, 8, 9), (8, 8, 16), (8, 1, 2),
                                             (16, 8, 11), (32, 8, 17), (8, 2, 40), (12, 3, 33),
-                                            (4, 1, 64), (8, 8, 130)])
+                                            (4, 1, 64), (8, 8, 130), (8, 8, 192), (32, 8, 50),
+                                            (8, 1, 33), (3, 3, 300), (16, 2, 24)])
 def test_decode_shared_prefixes(cuda, hq, hkv, members):
     rng = np.random.default_rng(hq + 10 * hkv + members)
     prefixes = (300, 33)
@@ -227,7 +229,8 @@ def test_decode_shared_prefixes(cuda, hq, hkv, members):
     q, o, lse, ws, _ = run_decode(pool, rng, lens, grp, prefixes)
     pick = None if members < 20 else [0, 1, members - 1, members, 2 * members - 1, 2 * members,
                                       2 * members + 1, 17, 18]
-    check_decode(pool, q, o, lse, lens, pick)
+    # a group of more than 128 rows runs on the extend's kernel, with its weights' rounding
+    check_decode(pool, q, o, lse, lens, pick, EXT_ERR if members * hq // hkv > 128 else DEC_ERR)
     assert rx.read_status(ws) == rx.RX_OK
 
 
@@ -238,6 +241,28 @@ def test_decode_long_requests_split_over_many_items(cuda):
     pool = Pool(cuda, rng, 8, 2, n, random_table(rng, n, lens))
     q, o, lse, _, plan = run_decode(pool, rng, lens)
     check_decode(pool, q, o, lse, lens)
+
+
+def test_decode_nan_and_out_of_pool_keys_in_the_prefix_of_a_very_large_group(cuda):
+    rng = np.random.default_rng(60)
+    members, prefix = 70, 200
+    lens = [prefix + 5] * members + [30]
+    pool = Pool(cuda, rng, 8, 2, 1500, random_table(rng, 1500, lens, {0: (list(range(members)),
+                                                                          prefix)}))
+    grp = [0] * members + [-1]
+    clean = run_decode(pool, rng, lens, grp, [prefix])
+    check_decode(pool, *clean[:3], lens, [0, 35, 69, 70], EXT_ERR)
+    pool.vs[pool.table[0, 131], 0] = np.nan
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, grp, [prefix], q=clean[0])
+    assert torch.isnan(o[:members, :4].float()).all() and torch.isfinite(lse).all()
+    assert torch.equal(o[:members, 4:], clean[1][:members, 4:]) and torch.equal(o[70], clean[1][70])
+    pool.vs[pool.table[0, 131], 0] = 1
+    pool.table[:members, 64] = 1500
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, grp, [prefix], q=clean[0])
+    assert rx.read_status(ws) == rx.RX_ERR_RANGE
+    check_decode(pool, q, o, lse, lens, [0, 69, 70], EXT_ERR)
 
 
 def test_decode_tree_and_grouping_give_the_same_result(cuda):
@@ -475,7 +500,6 @@ def test_two_streams_and_a_captured_graph(cuda):
 
 # ---- extend -----------------------------------------------------------------------------------
 
-EXT_ERR = 2.0 ** -8 + 2.0 ** -24  # bf16 weights, the V scale's product
 
 
 def run_extend(pool, rng, prefix, new, group_of_req=None, group_prefix_len=None,

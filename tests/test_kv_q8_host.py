@@ -172,6 +172,15 @@ def test_decode_plan_for_the_8_bit_pool_reads_each_key_as_often_as_its_units(lib
     assert plan.launches() == 2 and plan.rows() == members + 2
 
 
+def test_decode_plan_for_very_large_groups_reads_their_prefix_once(librx):
+    desc = _desc(32, 8, pool=1 << 20, rows=512, stride=4096)
+    for members, reads, launches in ((16, 1, 3), (17, 2, 3), (32, 2, 3), (33, 1, 4), (300, 1, 4)):
+        plan = _decode_plan(rx.RX_KV_E4M3, desc, [3000 + 10] * members,
+                            group_of_req=[0] * members, group_prefix_len=[3000])
+        assert plan.key_reads() == (3000 * reads + 10 * members) * 8, members
+        assert plan.launches() == launches, members
+
+
 def test_decode_plan_checks_are_those_of_the_bf16_pool(librx):
     desc = _desc()
     for seq in ([0], [513], [-1]):
