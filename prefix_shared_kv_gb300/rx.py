@@ -57,6 +57,7 @@ class KVDesc(C.Structure):
 class KVQ8(C.Structure):
     _fields_ = [("k_code", C.c_void_p), ("v_code", C.c_void_p), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p)]
+    tensors, shape, device = (), None, None  # of one made by kv_q8()
 
 
 _lib = None
@@ -227,32 +228,27 @@ def kv_q8(k_code, v_code, k_scale, v_scale) -> KVQ8:
     return kv
 
 
-def _fits(t, n: int, dtype, device: int) -> bool:
-    """Whether a tensor has n contiguous elements of dtype on the device; raw addresses (ints) are
-    the caller's responsibility."""
-    try:
-        return (t.numel() == n and t.dtype is dtype and t.get_device() == device
-                and t.is_contiguous())
-    except AttributeError:
-        return t is None or type(t) is int
-
-
 def _call_q8(fn, desc: KVDesc, kv: KVQ8, named, args, stream):
     """fn(*args, stream) after checking an 8-bit call's tensors: the pool's shape against the
-    descriptor, (name, tensor, elements, dtype) each, and that all are on the current device.  For a
-    hand-made KVQ8 the pool's shape and device are the caller's responsibility."""
+    descriptor, (name, tensor, elements, dtype) each, and that all are on the current device.  Raw
+    addresses (ints), and the pool of a hand-made KVQ8, are the caller's responsibility."""
     import torch
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() or _has_cuda() else -1
-    shape = getattr(kv, "shape", None)
-    if shape is not None:
-        if shape != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
-            raise ValueError(f"the pool is {shape}, the descriptor's "
+    if kv.shape is not None:
+        if kv.shape != (desc.pool_size, desc.num_kv_heads, desc.head_dim):
+            raise ValueError(f"the pool is {kv.shape}, the descriptor's "
                              f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
-        if kv.device != device or device < 0:
-            raise ValueError(f"the pool is on device {kv.device}, the current CUDA device is "
-                             f"{device}")
+        if kv.device < 0:
+            raise ValueError("the pool's tensors are not CUDA tensors")
+        device = torch._C._cuda_getDevice()
+        if kv.device != device:
+            raise ValueError(f"the pool is on device {kv.device}, the current device is {device}")
+    else:
+        device = torch.cuda.current_device() if torch.cuda.is_available() else -1
     for name, t, n, dtype in named:
-        if not _fits(t, n, dtype, device):
+        if t is None or type(t) is int:
+            continue
+        if (t.numel() != n or t.dtype is not dtype or t.get_device() != device
+                or not t.is_contiguous()):
             raise ValueError(f"{name}: {n} contiguous elements of {dtype} on CUDA device {device} "
                              f"expected, got {t.numel()} of {t.dtype} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
@@ -260,11 +256,6 @@ def _call_q8(fn, desc: KVDesc, kv: KVQ8, named, args, stream):
             else _stream(stream))
     if st != RX_OK:
         _check(st)
-
-
-def _has_cuda() -> bool:
-    import torch
-    return torch.cuda.is_available()
 
 
 def store_kv_q8(desc: KVDesc, kv: KVQ8, k_new, v_new, slots, stream=None):
