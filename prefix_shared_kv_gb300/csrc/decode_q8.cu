@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
 // a partial whose log-sum-exp is NaN makes both NaN.
 // What bounds it is the latency of its reads, so a warp has kRows partial rows in flight: one after
 // another (a branch on the weight around each read) the call on 16,411 keys of one request took
-// 12.7 us instead of 11.3.  Eight rows instead of four cost a warp with few partials 1 to 2 %.
+// 12.7 us instead of 11.3; the first references fetched beside the kernel before, 10.8.  Eight rows
+// instead of four cost a warp with few partials 1 to 2 %.
 constexpr int merge_warps(int w) { return w > 8 ? w : 8; }  // warps of a CTA
 template <int W>
 __global__ void __launch_bounds__(32 * merge_warps(W)) merge_q8_kernel(
@@ -660,6 +661,9 @@ __global__ void __launch_bounds__(32 * merge_warps(W)) merge_q8_kernel(
   const int r_begin = merge_idx[b], n = live ? merge_idx[b + 1] - r_begin : 0;
   float mx = -CUDART_INF_F, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // (the plan was complete before the kernels of this call began, its partials are not)
+  DecMergeRef first{0, 0, 0, 0};
+  if (w + W * lane < n) first = refs[r_begin + w + W * lane];
   wait_for_predecessors();  // the partials are complete
   let_successors_start();
   // per chunk the lanes fetch one reference and log-sum-exp each, so every weight is known before
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(32 * merge_warps(W)) merge_q8_kernel(
     int64_t idx = 0;
     float li = -CUDART_INF_F;
     if (i < n) {
-      const DecMergeRef rf = refs[r_begin + i];
+      const DecMergeRef rf = c0 == w ? first : refs[r_begin + i];
       idx = (int64_t)rf.part + (int64_t)hk * rf.rows_real + rf.row + g;
       li = part_lse[idx];
     }
