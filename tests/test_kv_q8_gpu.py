@@ -243,6 +243,29 @@ def test_decode_long_requests_split_over_many_items(cuda):
     check_decode(pool, q, o, lse, lens)
 
 
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (1, 1, [20000, 1]),            # more than 32 partials for each of sixteen warps
+    (2, 1, [70000, 1, 257]),
+    (16, 16, [16001] + [40] * 24),  # many rows, one with many partials: eight warps each
+    (1, 1, [9000] + [1] * 400),
+    (4, 2, [300, 700, 1, 5])])
+def test_decode_merges_any_number_of_partials(cuda, hq, hkv, lens):
+    """The number of warps that merge a row follows its partials and the rows; half of the long
+    request's keys have weights of 2^-200 and less, so that whole partials weigh nothing."""
+    rng = np.random.default_rng(len(lens) + hq)
+    n = sum(lens) + 9
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens))
+    q = W.normal_bf16(rng, (len(lens), hq, 128))
+    far = pool.table[0, :lens[0] // 2]
+    # codes of the largest size, their sign against the first query head of each KV head
+    pool.kc[far] = np.where(A.bf16_to_f64(q[0, ::hq // hkv]) < 0, 0x7E, 0xFE)
+    pool.ks[far] *= 8
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, q=q)
+    check_decode(pool, q, o, lse, lens, range(min(len(lens), 5)))
+    assert rx.read_status(ws) == rx.RX_OK
+
+
 def test_decode_nan_and_out_of_pool_keys_in_the_prefix_of_a_very_large_group(cuda):
     rng = np.random.default_rng(60)
     members, prefix = 70, 200
