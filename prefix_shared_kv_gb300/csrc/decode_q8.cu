@@ -201,42 +201,6 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-// The queries of a consumer warp in an item, and their power of two.
-template <int NT, bool WIDE, int HBL>
-struct Queries {
-  using F = Form<WIDE, HBL>;
-  const Params& p;
-  const DecItem& it;
-  int kw, row0, head, rows;  // the warp's 32-key run of a stage, first row, KV head; the item's rows
-  __device__ Queries(const Params& p_, const DecItem& it_) : p(p_), it(it_) {
-    const int warp = threadIdx.x >> 5;
-    kw = warp % (kWarps / F::kRowWarps);
-    row0 = warp / (kWarps / F::kRowWarps) * (8 * NT);
-    head = it.head_block * F::HB + (kw & (F::HB - 1));
-    rows = it.n_tok * p.gq;
-  }
-  // This lane's part of row row0 + 8 n + lane / 4: d = 16 k + 4 (lane % 4) .. + 3 for k = 0 .. 7.
-  __device__ void load(int n, uint2 (&x)[8]) const {
-    const int r = row0 + 8 * n + ((threadIdx.x & 31) >> 2);
-    const __nv_bfloat16* src =
-        p.q + ((int64_t)(r < rows ? __ldg(p.rows + it.row_begin + r / p.gq) : 0) * p.hq +
-               head * p.gq + r % p.gq) * kHeadDim + 4 * (threadIdx.x & 3);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      x[k] = r < rows ? __ldg(reinterpret_cast<const uint2*>(src + 16 * k)) : make_uint2(0, 0);
-  }
-  // Biased exponent of the row's largest magnitude (255: not finite; of a row below 2^-87, 40).
-  static __device__ int exponent(const uint2 (&x)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      m = __vmaxu2(m, __vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    return max((int)(max(m & 0xffffu, m >> 16) >> 7), 40);
-  }
-};
-
 // The partial result of one query row over the warp's keys of an item, in fp32, without the ring: a
 // lane takes a key's score, then four of the 128 columns.
 template <bool WIDE, int HBL>
@@ -608,6 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Params p) 
     *abort = 0;
   }
   __syncthreads();
+  // (the plan is older than every kernel that this one may start beside; one request of 16,411 keys
+  // 13.4 us instead of 13.7, 64 rows a head on 16,000 keys 280 instead of 285)
+  if (const int first = item_at(p, 0); first >= 0)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.items + first));
   // A narrow kernel behind a wide one starts beside it: the wide one's CTAs have all passed this
   // wait by then, so what came before the call is complete.
   if (WIDE || !p.after_wide) wait_for_predecessors();
@@ -856,10 +824,10 @@ int launch_merge_q8(const rx_kv_desc* d, const PlanHeader* h, int32_t n, void* o
   const uint8_t* base = static_cast<const uint8_t*>(ws);
   const int hq = d->num_q_heads, gq = hq / d->num_kv_heads;
   cudaStream_t s = (cudaStream_t)stream;
-  // One warp a row up to 8 partials, two up to 32, else eight; sixteen when there are no more rows
-  // than two CTAs on each SM (52 rows of some 130 partials: the call takes 12.6 us, with eight warps
-  // 14.5; 1,216 rows: 37.5 us, with eight 25.8)
-  const bool few = (int64_t)n * hq <= 304;
+  // One warp a row up to 8 partials, two up to 32, else eight; sixteen for no more rows than SMs (52
+  // rows of some 130 partials: the call takes 12.6 us, with eight warps 14.5; 300 rows: 40.0 us, with
+  // eight 38.0)
+  const bool few = (int64_t)n * hq <= 152;
   return (int)(h->max_refs <= 8    ? launch_merge<1>(base, h, n, hq, gq, o, lse, s)
                : h->max_refs <= 32 ? launch_merge<2>(base, h, n, hq, gq, o, lse, s)
                : few               ? launch_merge<16>(base, h, n, hq, gq, o, lse, s)

@@ -31,7 +31,9 @@ cudaError_t launch_beside(void (*kernel)(P...), dim3 grid, dim3 block, size_t sm
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // reported here, not by the caller's next check
+  return e;
 }
 
 }  // namespace rx
