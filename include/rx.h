@@ -153,8 +153,8 @@ rx_status rx_plan_set_extend_kernel(rx_plan* plan, int32_t kernel);
 rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
  * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge; over
- * an 8-bit pool an extend launches two, expansion and attention, and a merge if its keys are split,
- * a decode up to five: expansion and attention of very large groups, wide items, narrow items,
+ * an 8-bit pool an extend launches two, expansion and attention, and a merge if tiles' keys are
+ * split, a decode up to five: expansion and attention of very large groups, wide items, narrow items,
  * merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
 rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches);
@@ -214,7 +214,9 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  * The call first expands each distinct key of the plan into its workspace, once for all the query
  * tiles that read it: rx_plan_workspace_size is about 522 bytes per distinct key and KV head (each
  * shared prefix and each request's own keys rounded up to 64).  A batch whose tiles would leave SMs
- * idle (a few new tokens on a long prefix) has the tiles' keys split over the SMs and merged. */
+ * idle (a few new tokens on a long prefix) has the tiles' keys split over the SMs and merged, one
+ * whose SMs would end far apart those of some tiles; each part of a row and query head so split takes
+ * 516 bytes of workspace. */
 rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream);

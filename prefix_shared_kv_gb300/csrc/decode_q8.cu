@@ -617,14 +617,18 @@ template <int W>
 __global__ void __launch_bounds__(32 * merge_warps(W)) merge_q8_kernel(
     const float* __restrict__ part_o, const float* __restrict__ part_lse,
     const int32_t* __restrict__ merge_idx, const DecMergeRef* __restrict__ refs, int batch, int hq,
-    int gq, __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+    int gq, const MergeRow* __restrict__ out, __nv_bfloat16* __restrict__ o,
+    float* __restrict__ lse) {
   constexpr int kMergeWarps = merge_warps(W), kRows = W == 1 ? 4 : 8;
   __shared__ float4 s_acc[kMergeWarps][32];
   __shared__ float s_max[kMergeWarps], s_tot[kMergeWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, w = warp % W;
   const int64_t task = (int64_t)blockIdx.x * (kMergeWarps / W) + warp / W;
-  const bool live = task < (int64_t)batch * hq;
-  const int b = live ? (int)(task / hq) : 0, h = live ? (int)(task % hq) : 0;
+  // an entry of the merge index holds one row's partials, for all its query heads, or (out) those of
+  // one KV head
+  const int heads = out ? gq : hq;
+  const bool live = task < (int64_t)batch * heads;
+  const int b = live ? (int)(task / heads) : 0, h = live ? (int)(task % heads) : 0;
   const int hk = h / gq, g = h % gq;
   const int r_begin = merge_idx[b], n = live ? merge_idx[b + 1] - r_begin : 0;
   float mx = -CUDART_INF_F, tot = 0.f;
@@ -715,9 +719,11 @@ __global__ void __launch_bounds__(32 * merge_warps(W)) merge_q8_kernel(
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   const uint2 packed =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2*>(o + ((int64_t)b * hq + h) * kHeadDim + lane * 4) = packed;
+  int64_t row = (int64_t)b * hq + h;
+  if (out) row = (int64_t)out[b].q_row * hq + out[b].kv_head * gq + g;
+  *reinterpret_cast<uint2*>(o + row * kHeadDim + lane * 4) = packed;
   if (lane == 0)
-    lse[(int64_t)b * hq + h] =
+    lse[row] =
         tot == 0.f ? -CUDART_INF_F
                    : ((mx == -CUDART_INF_F ? 0.f : mx) + __log2f(tot)) * 0.69314718055994530942f;
 }
@@ -726,7 +732,8 @@ template <int W>
 cudaError_t launch_merge(const uint8_t* base, const PlanHeader* h, int32_t n, int hq, int gq,
                          void* o, float* lse, cudaStream_t stream) {
   constexpr int kMergeWarps = merge_warps(W);
-  const int64_t tasks = (int64_t)n * hq;
+  const bool listed = h->n_merge_rows > 0;
+  const int64_t tasks = (int64_t)n * (listed ? gq : hq);
   return launch_beside(merge_q8_kernel<W>,
                        dim3((unsigned)((tasks + kMergeWarps / W - 1) / (kMergeWarps / W))),
                        dim3(32 * kMergeWarps), 0, stream,
@@ -734,6 +741,8 @@ cudaError_t launch_merge(const uint8_t* base, const PlanHeader* h, int32_t n, in
                        reinterpret_cast<const float*>(base + h->off_part_lse),
                        reinterpret_cast<const int32_t*>(base + h->off_merge_idx),
                        reinterpret_cast<const DecMergeRef*>(base + h->off_merge), (int)n, hq, gq,
+                       listed ? reinterpret_cast<const MergeRow*>(base + h->off_merge_rows)
+                              : nullptr,
                        static_cast<__nv_bfloat16*>(o), lse);
 }
 
@@ -824,6 +833,7 @@ int launch_merge_q8(const rx_kv_desc* d, const PlanHeader* h, int32_t n, void* o
   const uint8_t* base = static_cast<const uint8_t*>(ws);
   const int hq = d->num_q_heads, gq = hq / d->num_kv_heads;
   cudaStream_t s = (cudaStream_t)stream;
+  if (h->n_merge_rows > 0) n = (int32_t)h->n_merge_rows;
   // One warp a row up to 8 partials, two up to 32, else eight; sixteen for no more rows than SMs (52
   // rows of some 130 partials: the call takes 12.6 us, with eight warps 14.5; 300 rows: 40.0 us, with
   // eight 38.0)

@@ -730,11 +730,13 @@ static __device__ __forceinline__ void write_rows(const ExtParams& p, int idx, c
   // (8-bit pool: a NaN sum, from a NaN scale, is passed on)
   const bool none = Q8 ? l == 0.f : !(l > 0.f);
   const float inv = none ? 0.f : 1.f / l;
-  const bool partial = p.part_o != nullptr;
+  bool partial = p.part_o != nullptr;
   int64_t prow = 0;
   if (partial) {
     const ExtItem& itg = p.items[idx];
-    prow = (int64_t)__ldg(x ? &itg.part[1] : &itg.part[0]) + r;
+    const int32_t part = __ldg(x ? &itg.part[1] : &itg.part[0]);
+    if constexpr (Q8) partial = part >= 0;  // (a plan with some items cut: the others write o)
+    prow = (int64_t)part + r;
   }
   __nv_bfloat16* dst = p.o + ((int64_t)row.q_row * p.hq + row.qh) * kHeadDim;
   float* pdst = p.part_o + prow * kHeadDim;
@@ -1070,7 +1072,8 @@ int launch_extend_q8(const rx_kv_desc* d, const PlanHeader* h, const rx_kv_q8* k
   const int e = launch_expand_q8(d, kv, reinterpret_cast<const Q8Tile*>(base + h->off_q8_tiles),
                                  h->n_q8_tiles, base + h->off_q8_stage, status, stream);
   if (e) return e;
-  // a plan whose tiles do not fill the GPU splits their keys: partial rows, and a merge
+  // a plan whose tiles do not fill the GPU splits their keys, one whose lists of items end apart cuts
+  // some of them: partial rows, and a merge
   float* part_o = h->n_part_rows ? reinterpret_cast<float*>(base + h->off_part_o) : nullptr;
   float* part_lse = h->n_part_rows ? reinterpret_cast<float*>(base + h->off_part_lse) : nullptr;
   const int r = launch_items<true>(

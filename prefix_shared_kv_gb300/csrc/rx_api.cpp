@@ -157,6 +157,50 @@ int32_t attn_steps(int64_t n) { return (int32_t)((n + kAttnKeys - 1) / kAttnKeys
 int64_t attn_cost(const ExtItem& it) { return (int64_t)it.n_steps * (it.n_tok[1] > 0 ? 14 : 11); }
 constexpr int64_t kItemCost = 66;
 
+// 8-bit pool: an item's last `steps` steps, given to CTA `to`.
+struct Cut {
+  int32_t item, steps, to;
+};
+// A cut costs its two pieces' partial rows about two steps, and the plan a merge (5 us, and what it
+// takes to write and read the rows), in the units of attn_cost.  The figures were fitted over 60 random
+// batches: five groups of six requests with 1 to 9 new tokens on 5,169, 16 heads, 145 us without
+// cuts, 123 with; five groups of nine with up to 1,365 on 986, one head, 86 and 65; a chunk of 2,048
+// new tokens on 5,120, 32/8 heads, 229 and 232: not cut.
+constexpr int64_t kCutCost = 28, kMergeCost = 75, kMergeRowsPerCost = 160;
+constexpr int32_t kLeastPiece = 4;  // steps
+
+// Cuts by which every list ends at `end` or before: each that ends later gives the end of its longest
+// item to the one with most room.  False when that does not do.
+bool cut_lists(const std::vector<ExtItem>& items, const std::vector<std::vector<int32_t>>& lists,
+               const std::vector<int64_t>& load, int64_t end, std::vector<Cut>& cuts) {
+  cuts.clear();
+  std::priority_queue<std::pair<int64_t, int32_t>> room;
+  std::vector<std::pair<int64_t, int32_t>> late;
+  for (int32_t k = 0; k < (int32_t)load.size(); ++k)
+    if (load[k] > end)
+      late.push_back({load[k] - end, k});
+    else
+      room.push({end - load[k], k});
+  std::sort(late.begin(), late.end(), std::greater<std::pair<int64_t, int32_t>>());
+  for (const auto& l : late) {
+    int32_t longest = lists[l.second][0];
+    for (int32_t i : lists[l.second])
+      if (items[i].n_steps > items[longest].n_steps) longest = i;
+    const ExtItem& it = items[longest];
+    const int64_t step = it.n_tok[1] > 0 ? 14 : 11;
+    const int32_t n =
+        (int32_t)std::max<int64_t>(kLeastPiece, (l.first + kCutCost + step - 1) / step);
+    if (it.n_steps - n < kLeastPiece || room.empty()) return false;
+    const auto to = room.top();
+    const int64_t left = to.first - (n * step + kItemCost + kCutCost);
+    if (left < 0) return false;
+    room.pop();
+    room.push({left, to.second});
+    cuts.push_back({longest, n, to.second});
+  }
+  return true;
+}
+
 // SMs of the calling thread's current GPU, the number of per-CTA lists an extend plan for the
 // one-SM kernel makes; a GB300's 152 where no GPU can be asked (plans are host work).
 int32_t plan_sm_count() {
@@ -1225,6 +1269,7 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   }
   std::vector<int32_t> midx;
   std::vector<DecMergeRef> mref;
+  std::vector<MergeRow> merge_rows;
   int32_t max_refs = 0;
   if (split_steps) {
     midx.push_back(0);
@@ -1250,7 +1295,10 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
     // order start at about the same time on different SMs -- the tiles of one unit read its
     // prefix and its causal keys while they are in L2 -- and the lists end at about the same
     // time.  The table is stored CTA by CTA.
-    const int32_t G = (int32_t)std::min<int64_t>(plan_sm_count(), (int64_t)items.size());
+    // (8-bit pool: a list for every SM, so that cut items can fill those without an item)
+    const int32_t G = q8 && !split_steps
+                          ? plan_sm_count()
+                          : (int32_t)std::min<int64_t>(plan_sm_count(), (int64_t)items.size());
     using Slot = std::pair<int64_t, int32_t>;  // (end of the list, CTA)
     std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>> free_at;
     for (int32_t k = 0; k < G; ++k) free_at.push({0, k});
@@ -1290,10 +1338,80 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       load[hi] -= cost_of(i);
       load[lo] += cost_of(i);
     }
+    // 8-bit pool: where the lists end apart all the same (a few items each), those that end late
+    // give the last steps of their longest item to those that end early.  Both pieces of such an
+    // item leave partial rows for a merge.
+    if (q8 && !split_steps) {
+      const int64_t before = *std::max_element(load.begin(), load.end());
+      int64_t lo = 0;
+      for (int64_t x : load) lo += x;
+      lo /= G;  // no schedule ends before
+      std::vector<Cut> cuts, best_cuts;
+      int64_t after = before;
+      while (after - lo > 1) {
+        const int64_t end = lo + (after - lo) / 2;
+        if (cut_lists(items, lists, load, end, cuts)) {
+          after = end;
+          best_cuts.swap(cuts);
+        } else {
+          lo = end;
+        }
+      }
+      int64_t cut_rows = 0;
+      for (const Cut& c : best_cuts)
+        cut_rows += (int64_t)(items[c.item].n_tok[0] + items[c.item].n_tok[1]) * gq;
+      if (before - after > kMergeCost + cut_rows / kMergeRowsPerCost &&
+          npart + 2 * cut_rows <= (int64_t)INT32_MAX) {
+        for (ExtItem& it : items) it.part[0] = it.part[1] = -1;
+        midx.push_back(0);
+        for (const Cut& c : best_cuts) {
+          ExtItem tail = items[c.item];
+          ExtItem& head = items[c.item];
+          // the tail's segments: a part of the one it starts in, and those behind
+          int32_t at = head.seg_begin, skip = head.n_steps - c.steps;
+          for (; skip >= attn_steps(segs[at].k_end - segs[at].k_begin); ++at)
+            skip -= attn_steps(segs[at].k_end - segs[at].k_begin);
+          const int32_t behind = head.seg_begin + head.n_seg;
+          const int32_t shared = skip > 0;  // the segment at which both pieces take a part
+          const int32_t first = (int32_t)segs.size();
+          for (int32_t j = head.seg_begin; j < at + shared; ++j) segs.push_back(segs[j]);
+          tail.seg_begin = (int32_t)segs.size();
+          for (int32_t j = at; j < behind; ++j) segs.push_back(segs[j]);
+          if (shared) {
+            const int32_t k = segs[at].k_begin + skip * kAttnKeys;
+            segs[tail.seg_begin - 1].k_end = k;
+            segs[tail.seg_begin].k_begin = k;
+            segs[tail.seg_begin].kv_row += skip;
+          }
+          head.seg_begin = first;
+          head.n_seg = tail.seg_begin - first;
+          head.n_steps -= c.steps;
+          tail.n_seg = (int32_t)segs.size() - tail.seg_begin;
+          tail.n_steps = c.steps;
+          for (int x = 0; x < 2; ++x) {
+            const int32_t n = head.n_tok[x];
+            if (n == 0) continue;
+            head.part[x] = (int32_t)npart;
+            tail.part[x] = (int32_t)(npart + (int64_t)n * gq);
+            for (int32_t i = 0; i < n; ++i) {
+              mref.push_back({head.part[x] + i * gq, 0, 0, 0});
+              mref.push_back({tail.part[x] + i * gq, 0, 0, 0});
+              midx.push_back((int32_t)mref.size());
+              merge_rows.push_back({rows[head.row_begin[x] + i].q_row, head.kv_head});
+            }
+            npart += 2 * (int64_t)n * gq;
+          }
+          max_refs = 2;
+          lists[c.to].push_back((int32_t)items.size());
+          items.push_back(tail);
+        }
+      }
+    }
     std::vector<ExtItem> by_cta;
     by_cta.reserve(items.size());
     cta_begin.push_back(0);
     for (const auto& l : lists) {
+      if (l.empty()) continue;
       for (int32_t i : l) by_cta.push_back(items[i]);
       cta_begin.push_back((int32_t)by_cta.size());
     }
@@ -1321,6 +1439,8 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   h.n_q8_tiles = (int32_t)tiles8.size();
   h.off_merge_idx = off; off = align256(off + midx.size() * 4);
   h.off_merge = off; off = align256(off + mref.size() * sizeof(DecMergeRef));
+  h.off_merge_rows = off; off = align256(off + merge_rows.size() * sizeof(MergeRow));
+  h.n_merge_rows = (int64_t)merge_rows.size();
   h.max_refs = max_refs;
   plan->blob.assign(off, 0);
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
@@ -1336,6 +1456,7 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   put(plan->blob, h.off_q8_tiles, tiles8);
   put(plan->blob, h.off_merge_idx, midx);
   put(plan->blob, h.off_merge, mref);
+  put(plan->blob, h.off_merge_rows, merge_rows);
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 1;

@@ -115,11 +115,17 @@ struct ExtItem {
   int32_t n_seg;
   int32_t kv_head;
   int32_t n_steps;       // 64-key steps over the segments (each segment's keys rounded up)
-  int32_t part[2];       // decode plans: first partial row of each tile; unused for extend
+  // first partial row of each tile: decode plans, and extend plans for the 8-bit pool that have partial
+  // rows (there -1: the item writes its rows' results); unused for the other extend plans
+  int32_t part[2];
 };
 
 // Workspace layout written by rx_plan_upload: a 256-byte header, then the tables, then (decode)
 // the partial outputs.  Offsets are in bytes from the workspace base and 256-byte aligned.
+// A token row's query heads of one KV head, for a merge of the 8-bit pool's extend.
+struct MergeRow {
+  int32_t q_row, kv_head;
+};
 struct PlanHeader {
   uint32_t magic;
   int32_t kind;          // 1 = extend, 2 = decode
@@ -148,7 +154,11 @@ struct PlanHeader {
   // decode plans for the 8-bit pool: wide items and their per-CTA lists
   int64_t off_wide, off_wide_cta;
   int32_t n_wide, n_wide_ctas;
-  int64_t pad[7];
+  // extend plans for the 8-bit pool of which some items are cut: the rows that the merge writes, as
+  // MergeRow (n_merge_rows = 0: it writes every row, each by its entry of the merge index)
+  int64_t off_merge_rows;
+  int64_t n_merge_rows;
+  int64_t pad[5];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
 

@@ -628,6 +628,47 @@ def test_extend_small_batches_with_a_shared_prefix_split_their_keys(cuda):
     check_extend(pool, q, o, lse, prefix, new)
 
 
+@pytest.mark.parametrize("hq,hkv,prefix,new,groups,parents", [
+    (64, 8, [4000], [340], [], None),          # fewer pairs of tiles than SMs, more tiles
+    (24, 3, [2500], [830], [], None),
+    (8, 1, [0], [4000], [], None),             # nothing cached: causal tiles of every length
+    (16, 2, [4000, 100], [1250, 33], [], None),
+    (20, 5, [2000] * 3, [300, 2, 700], [(0, 1, 2)], None),
+    (40, 5, [3000] * 4, [130, 165, 200, 1], [(0, 1), (2,), (3,)], [-1, 0, 0])])
+def test_extend_cuts_items_where_the_lists_end_apart(cuda, hq, hkv, prefix, new, groups, parents):
+    """Batches of one to three items an SM: some items are cut, their rows merged, the others write
+    theirs; the whole result twice, bit for bit."""
+    rng = np.random.default_rng(hq + len(new))
+    lens = [p + e for p, e in zip(prefix, new)]
+    n = sum(lens) + 20
+    shared = {0: (list(range(len(new))), prefix[0])} if groups else None
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens, shared))
+    grp, gpl = None, None
+    if groups:
+        grp = [next(g for g, m in enumerate(groups) if b in m) for b in range(len(new))]
+        gpl = [prefix[0]] if parents is None else [600, 2500, 2500]
+    rows = int(np.sum(new))
+    q = W.normal_bf16(rng, (rows, hq, 128))
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    rx.extend_plan(plan, pool.desc, np.arange(len(new)), prefix, new, grp, gpl, parents)
+    assert plan.launches() == 3
+    ws = workspace(plan.workspace_size(), cuda)
+    results = []
+    for fill in (0xFF, 0x00):  # partials that the merge reads without a write would be NaN
+        ws.fill_(fill)
+        plan.upload(ws)
+        o = torch.full((rows + 1, hq, 128), 7.0, dtype=torch.bfloat16, device=cuda)
+        lse = torch.full((rows + 1, hq), 7.0, device=cuda)
+        rx.extend_attn_q8(plan, pool.desc, pool.kv, to_bf16(q, cuda), o[:rows], lse[:rows], ws)
+        torch.cuda.synchronize()
+        assert rx.read_status(ws) == rx.RX_OK
+        assert (o[rows] == 7).all() and (lse[rows] == 7).all()
+        results.append((o, lse))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    check_extend(pool, q, o[:rows], lse[:rows], prefix, new)
+
+
 def test_extend_every_code_and_scale(cuda):
     """Codes of every value (subnormal ones too) and scales over 2^60."""
     prefix, new = [254], [64]
