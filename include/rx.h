@@ -154,7 +154,7 @@ rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
  * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge; over
  * an 8-bit pool an extend launches two, expansion and attention, and a merge if tiles' keys are
- * split, a decode up to five: expansion and attention of very large groups, wide items, narrow items,
+ * split, one of few new tokens what a decode does; a decode up to five: expansion and attention of very large groups, wide items, narrow items,
  * merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
 rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches);
@@ -211,7 +211,9 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
  * with fp32 sums of exact products of the codes.  Scales of keys a row does not see, NaN ones
  * included, do not reach it.  pool_size * num_kv_heads is not limited.
- * The call first expands each distinct key of the plan into its workspace, once for all the query
+ * A plan of few new tokens (at most 32 a request) that would be faster as a decode of them runs as
+ * rx_decode_attn_q8 does, each new token a request with the keys up to its own.  Otherwise
+ * the call first expands each distinct key of the plan into its workspace, once for all the query
  * tiles that read it: rx_plan_workspace_size is about 522 bytes per distinct key and KV head (each
  * shared prefix and each request's own keys rounded up to 64).  A batch whose tiles would leave SMs
  * idle (a few new tokens on a long prefix) has the tiles' keys split over the SMs and merged, one

@@ -107,6 +107,7 @@ struct rx_plan {
   std::vector<uint8_t> blob;  // header + tables, uploaded verbatim
   size_t ws_bytes = 0;
   int64_t key_reads = 0;  // (key, KV head) rows of the pool the kernels read
+  double q8_us = 0;       // decode plans for the 8-bit pool: the planner's estimate of a call
   int32_t hq = 0, hkv = 0;
   int64_t rows = 0, stride = 0, pool = 0;
   const int32_t* table = nullptr;
@@ -258,7 +259,7 @@ rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_k
       d->req_to_token_stride != p->stride || d->pool_size != p->pool)
     return fail(RX_ERR_INVALID, "descriptor differs from the one the plan was built with");
   const PlanHeader h = p->hdr();
-  if (h.n_items > 0 || (kind == 2 && h.batch > 0)) {  // an extend plan without new tokens has no rows
+  if (h.n_items > 0 || (h.kind == 2 && h.batch > 0)) {  // an extend plan without new tokens has no rows
     if (!k || !v || !q || !o || !lse) return fail(RX_ERR_INVALID, "NULL tensor pointer");
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(o) || !aligned16(lse))
       return fail(RX_ERR_INVALID, "tensors must be 16-byte aligned");
@@ -415,7 +416,7 @@ rx_status rx_plan_rows(const rx_plan* plan, int64_t* rows) {
   if (!plan || !rows) return fail(RX_ERR_INVALID, "NULL argument");
   if (!plan->kind) return fail(RX_ERR_INVALID, "plan has not been built");
   const PlanHeader h = plan->hdr();
-  *rows = plan->kind == 1 ? h.n_rows : h.batch;  // extend: one row per new token
+  *rows = h.kind == 1 ? h.n_rows : h.batch;  // extend: one row per new token
   return RX_OK;
 }
 
@@ -427,8 +428,8 @@ rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches) {
   // items; decode -- the tensor-core kernel for its shared-prefix units, the mma.sync partial
   // kernel for the others, and the merge whenever there are requests
   // (an extend over an 8-bit pool expands the plan's keys in a kernel of its own first, and merges
-  // when its tiles' keys are split)
-  *launches = plan->kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3) +
+  // when its tiles' keys are split, or runs as a decode of its few new tokens)
+  *launches = h.kind == 1 ? (h.n_items > 0) * (1 + (h.kv_type == RX_KV_E4M3) +
                                                    (h.n_part_rows > 0))
                               : (h.n_xitems > 0) * (1 + (h.kv_type == RX_KV_E4M3)) + (h.n_wide > 0) + (h.n_items > 0) + (h.batch > 0);
   return RX_OK;
@@ -628,6 +629,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   // hundred random batches: a start of 0.5 stages and 2 passes read 16 x 16 requests on 2,000-token
   // prefixes in 153 us instead of 155, but 126 requests of up to 542 tokens in 33.8 instead of 26.3.
   int q8_stages[2] = {1, 1};
+  int64_t q8_longest[2] = {0, 0};
   auto item_cost = [&](int kind, int n_rows, int stages) {  // in hundredths of a stage
     const int hb = hb_of(kind), rows_stage = kind == 2 ? 128 : 256;
     return 100ll * stages + 150 + 100ll * 3 * n_rows * hb * kHeadDim * 4 / (rows_stage * 264);
@@ -669,6 +671,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       }
       if (longest < best) {
         best = longest;
+        q8_longest[wide] = longest;
         q8_stages[wide] = (int)std::min<int64_t>(n, 1 << 16);
       }
     }
@@ -897,6 +900,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   put(plan->blob, h.off_q8_tiles, tiles8);
   put(plan->blob, h.off_wide, wide);
   put(plan->blob, h.off_wide_cta, wide_begin);
+  // a narrow stage takes 1.7 us (67 KB at the rate of an SM), a wide one 2.1 (its arithmetic)
+  plan->q8_us = 0.017 * q8_longest[0] + 0.021 * q8_longest[1];
   plan->ws_bytes = off;
   plan->key_reads = key_reads;
   plan->kind = 2;
@@ -961,6 +966,44 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
     return extend_plan_tree(plan, desc, batch, req_idx, prefix_len, extend_len, group_of_req,
                             num_groups, group_prefix_len, group_parent);
   });
+}
+
+// 8-bit pool: extends of at most this many new tokens, in all and of a request, are also planned as a
+// decode (16 requests of one or two new tokens in pairs on 5,715, 48/12 heads: 36.8 us, expanded and
+// on tiles 172; 10 of up to 17 on 715, 12/12 heads: 17.0 and 14.8, on tiles).
+constexpr int64_t kFewTokens = 2048;
+constexpr int32_t kFewPerRequest = 32;
+// A step's keys in the expansion (read, and written), and what an extend's launches take beyond a
+// decode's.
+constexpr double kQ8ExpandBytes = kAttnKeys * 264. + kQ8BlockBytes, kQ8ExtendUs = 1.;
+
+// The decode plan of an extend's new tokens: each a request of its own with the keys up to itself; a
+// request's cached keys are a node that its tokens share.
+static rx_status few_tokens_plan(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
+                                 const int32_t* req_idx, const int32_t* prefix_len,
+                                 const int32_t* extend_len, const std::vector<int>& grp,
+                                 int32_t num_groups, const int32_t* group_prefix_len,
+                                 const int32_t* group_parent) {
+  std::vector<int32_t> row, len, node, node_len, parent;
+  for (int32_t g = 0; g < num_groups; ++g) {
+    node_len.push_back(group_prefix_len[g]);
+    parent.push_back(group_parent ? group_parent[g] : -1);
+  }
+  for (int32_t b = 0; b < batch; ++b) {
+    int32_t at = grp[b];
+    if (extend_len[b] > 1 && prefix_len[b] > (at >= 0 ? node_len[at] : 0)) {
+      node_len.push_back(prefix_len[b]);
+      parent.push_back(at);
+      at = (int32_t)node_len.size() - 1;
+    }
+    for (int32_t i = 0; i < extend_len[b]; ++i) {
+      row.push_back(req_idx[b]);
+      len.push_back(prefix_len[b] + i + 1);
+      node.push_back(at);
+    }
+  }
+  return decode_plan_tree(plan, desc, (int32_t)row.size(), row.data(), len.data(), node.data(),
+                          (int32_t)node_len.size(), node_len.data(), parent.data());
 }
 
 static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t batch,
@@ -1105,41 +1148,6 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
             tiles8.push_back({sg.kv_row, k, std::min(kAttnKeys, w.first - k), 0});
         }
   }
-  // 8-bit pool: when the pairs of tiles below would leave SMs without work, the items are single
-  // tiles, and the steps of each tile are split over as many items as there are SMs for; such
-  // items leave partial rows, which a merge combines.  (In the units of attn_cost: writing a tile's
-  // partial rows costs about a step, the merge about 3 us.)  0: no split.
-  int32_t split_steps = 0;
-  auto tile_steps = [](const Tile& tl) {
-    int32_t n = 0;
-    for (const ExtSeg& sg : tl.segs) n += attn_steps(sg.k_end - sg.k_begin);
-    return n;
-  };
-  if (q8) {
-    const int64_t sms = plan_sm_count();
-    int64_t n_pairs = 0, n_tiles = 0, total = 0, most = 0;
-    for (const Unit& un : units) {
-      n_pairs += (int64_t)(un.tiles.size() + 1) / 2 * hkv;
-      n_tiles += (int64_t)un.tiles.size() * hkv;
-      for (const Tile& tl : un.tiles) {
-        total += (int64_t)tile_steps(tl) * hkv;
-        most = std::max<int64_t>(most, tile_steps(tl));
-      }
-    }
-    if (n_tiles > 0 && n_pairs < sms && n_tiles <= sms) {
-      int64_t c = std::max<int64_t>(2, (total + sms - 1) / sms);
-      auto count = [&](int64_t steps) {
-        int64_t n = 0;
-        for (const Unit& un : units)
-          for (const Tile& tl : un.tiles) n += (tile_steps(tl) + steps - 1) / steps * hkv;
-        return n;
-      };
-      while (c < most && count(c) > sms) ++c;
-      // a pair walks at least its longer tile, at the price of a two-tile step
-      if (c < most && 11 * c + 14 + 41 < 14 * most) split_steps = (int32_t)c;
-    }
-  }
-
   // Pair consecutive tiles of a unit (similar cost after the sort) into one item; the pair walks
   // the union of the two segment lists (same owner: the longer range).  An odd last tile is
   // paired with an empty one.
@@ -1167,6 +1175,73 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       segs.insert(segs.end(), u.begin(), u.end());
       pr.n_seg = (int)u.size();
       pairs[k].push_back(pr);
+    }
+  }
+
+  // 8-bit pool: when the pairs of tiles would leave SMs without work, the steps of each pair, or of
+  // each tile by itself, are split over as many items as there are SMs for; such items leave partial
+  // rows, which a merge combines.  (In the units of attn_cost: writing a tile's partial rows costs
+  // about a step, the merge about 3 us and its reads.  Pairs pass over the keys half as often, single
+  // tiles leave half as many partial rows: 155 new tokens on 8,049 in three groups, 64/16 heads, 96
+  // tiles: by tiles 190 us, by pairs 122; 129 on 4,007 in two, 24/3 heads: 29.7 and 33.1.)
+  struct Work {
+    int32_t row_begin[2], n_tok[2];
+    std::vector<ExtSeg> segs;
+    int32_t n_steps;
+  };
+  std::vector<Work> works;  // of the split
+  int32_t split_steps = 0;  // a split item's, 0: no split
+  if (q8) {
+    const int64_t sms = plan_sm_count();
+    auto works_of = [&](bool by_pairs) {
+      std::vector<Work> all;
+      for (size_t k = 0; k < units.size(); ++k) {
+        const auto& tiles = units[k].tiles;
+        auto add = [&](int a, int b, std::vector<ExtSeg> sg) {
+          Work w{{tiles[a].row_begin, b >= 0 ? tiles[b].row_begin : 0},
+                 {tiles[a].n_tok, b >= 0 ? tiles[b].n_tok : 0}, std::move(sg), 0};
+          for (const ExtSeg& x : w.segs) w.n_steps += attn_steps(x.k_end - x.k_begin);
+          all.push_back(std::move(w));
+        };
+        if (by_pairs)
+          for (const Pair& pr : pairs[k])
+            add(pr.a, pr.b, {segs.begin() + pr.seg_begin, segs.begin() + pr.seg_begin + pr.n_seg});
+        else
+          for (size_t i = 0; i < tiles.size(); ++i) add((int)i, -1, tiles[i].segs);
+      }
+      return all;
+    };
+    int64_t n_pairs = 0, longest = 0;
+    for (const auto& u : pairs) n_pairs += (int64_t)u.size() * hkv;
+    if (n_pairs > 0 && n_pairs < sms) {
+      int64_t best = INT64_MAX;
+      for (int by_pairs = 1; by_pairs >= 0; --by_pairs) {
+        std::vector<Work> all = works_of(by_pairs);
+        if ((int64_t)all.size() * hkv > sms) continue;
+        int64_t total = 0, most = 0;
+        for (const Work& w : all) {
+          total += (int64_t)w.n_steps * hkv;
+          most = std::max<int64_t>(most, w.n_steps);
+        }
+        if (by_pairs) longest = 14 * most;
+        auto count = [&](int64_t steps) {
+          int64_t n = 0;
+          for (const Work& w : all) n += (w.n_steps + steps - 1) / steps * hkv;
+          return n;
+        };
+        int64_t c = std::max<int64_t>(2, (total + sms - 1) / sms);
+        while (c < most && count(c) > sms) ++c;
+        int64_t partials = 0;
+        for (const Work& w : all)
+          partials += (w.n_steps + c - 1) / c * (w.n_tok[0] + w.n_tok[1]) * gq * hkv;
+        const int64_t cost =
+            (by_pairs ? 14 * c + 28 : 11 * c + 14) + partials / (2 * kMergeRowsPerCost);
+        if (c < most && cost < best && cost + 41 < longest) {
+          best = cost;
+          split_steps = (int32_t)c;
+          works = std::move(all);
+        }
+      }
     }
   }
 
@@ -1219,49 +1294,52 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   } else if (q8) {
     items.clear();
     segs.clear();
-    for (const Unit& un : units)
-      for (const Tile& tl : un.tiles) {
-        const int32_t steps = tile_steps(tl), parts = (steps + split_steps - 1) / split_steps;
-        const int32_t per = (steps + parts - 1) / parts;
-        size_t at = 0;
-        int32_t k0 = tl.segs[0].k_begin;
-        while (at < tl.segs.size()) {
-          ExtItem it;
-          std::memset(&it, 0, sizeof it);
-          it.row_begin[0] = tl.row_begin;
-          it.n_tok[0] = tl.n_tok;
-          it.seg_begin = (int32_t)segs.size();
-          for (int32_t left = per; left > 0 && at < tl.segs.size();) {
-            const ExtSeg& sg = tl.segs[at];
-            const int32_t n = std::min(left, attn_steps(sg.k_end - k0));
-            const int32_t end = std::min(sg.k_end, k0 + n * kAttnKeys);
-            segs.push_back({stage_of(sg).second + (k0 - sg.k_begin) / kAttnKeys, k0, end, sg.owner});
-            it.n_steps += n;
-            left -= n;
-            k0 = end;
-            if (k0 >= sg.k_end && ++at < tl.segs.size()) k0 = tl.segs[at].k_begin;
-          }
-          it.n_seg = (int32_t)segs.size() - it.seg_begin;
+    for (const Work& w : works) {
+      const int32_t parts = (w.n_steps + split_steps - 1) / split_steps;
+      const int32_t per = (w.n_steps + parts - 1) / parts;
+      size_t at = 0;
+      int32_t k0 = w.segs[0].k_begin;
+      while (at < w.segs.size()) {
+        ExtItem it;
+        std::memset(&it, 0, sizeof it);
+        it.seg_begin = (int32_t)segs.size();
+        for (int32_t left = per; left > 0 && at < w.segs.size();) {
+          const ExtSeg& sg = w.segs[at];
+          const int32_t n = std::min(left, attn_steps(sg.k_end - k0));
+          const int32_t end = std::min(sg.k_end, k0 + n * kAttnKeys);
+          segs.push_back({stage_of(sg).second + (k0 - sg.k_begin) / kAttnKeys, k0, end, sg.owner});
+          it.n_steps += n;
+          left -= n;
+          k0 = end;
+          if (k0 >= sg.k_end && ++at < w.segs.size()) k0 = w.segs[at].k_begin;
+        }
+        it.n_seg = (int32_t)segs.size() - it.seg_begin;
+        const int64_t first = npart;
+        for (int x = 0; x < 2; ++x) {
+          it.row_begin[x] = w.row_begin[x];
+          it.n_tok[x] = w.n_tok[x];
           // the rows that see one of the item's keys take its partial result
-          for (int i = 0; i < tl.n_tok; ++i) {
-            const ExtRow& row = rows[tl.row_begin + i];
+          for (int i = 0; i < w.n_tok[x]; ++i) {
+            const ExtRow& row = rows[w.row_begin[x] + i];
             bool sees = false;
             for (int j = 0; j < it.n_seg && !sees; ++j) {
               const ExtSeg& sg = segs[it.seg_begin + j];
               sees = (sg.owner < 0 || sg.owner == row.owner) && sg.k_begin < row.kmax;
             }
             if (sees)
-              refs[row.q_row].push_back({(int32_t)npart, tl.n_tok * gq, i * gq, 0});
+              refs[row.q_row].push_back({(int32_t)npart, w.n_tok[x] * gq, i * gq, 0});
           }
-          for (int h = 0; h < hkv; ++h) {
-            it.kv_head = h;
-            it.part[0] = (int32_t)(npart + (int64_t)h * tl.n_tok * gq);
-            items.push_back(it);
-          }
-          npart += (int64_t)hkv * tl.n_tok * gq;
+          npart += (int64_t)hkv * w.n_tok[x] * gq;
           if (npart > (int64_t)INT32_MAX) return fail(RX_ERR_RANGE, "plan too large");
         }
+        for (int h = 0; h < hkv; ++h) {
+          it.kv_head = h;
+          it.part[0] = (int32_t)(first + (int64_t)h * w.n_tok[0] * gq);
+          it.part[1] = (int32_t)(first + (int64_t)(hkv * w.n_tok[0] + h * w.n_tok[1]) * gq);
+          items.push_back(it);
+        }
       }
+    }
   }
   if (q8) {
     key_reads = 0;  // the pool is read by the expansion only
@@ -1271,6 +1349,7 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   std::vector<DecMergeRef> mref;
   std::vector<MergeRow> merge_rows;
   int32_t max_refs = 0;
+  int64_t ends_at = 0;  // of the longest list, in the units of attn_cost
   if (split_steps) {
     midx.push_back(0);
     for (const auto& r : refs) {
@@ -1338,11 +1417,12 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       load[hi] -= cost_of(i);
       load[lo] += cost_of(i);
     }
+    ends_at = *std::max_element(load.begin(), load.end());
     // 8-bit pool: where the lists end apart all the same (a few items each), those that end late
     // give the last steps of their longest item to those that end early.  Both pieces of such an
     // item leave partial rows for a merge.
     if (q8 && !split_steps) {
-      const int64_t before = *std::max_element(load.begin(), load.end());
+      const int64_t before = ends_at;
       int64_t lo = 0;
       for (int64_t x : load) lo += x;
       lo /= G;  // no schedule ends before
@@ -1362,6 +1442,7 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
         cut_rows += (int64_t)(items[c.item].n_tok[0] + items[c.item].n_tok[1]) * gq;
       if (before - after > kMergeCost + cut_rows / kMergeRowsPerCost &&
           npart + 2 * cut_rows <= (int64_t)INT32_MAX) {
+        ends_at = after;
         for (ExtItem& it : items) it.part[0] = it.part[1] = -1;
         midx.push_back(0);
         for (const Cut& c : best_cuts) {
@@ -1416,6 +1497,27 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
       cta_begin.push_back((int32_t)by_cta.size());
     }
     items.swap(by_cta);
+  }
+
+  // 8-bit pool: a few new tokens a request are a decode of as many rows, each with the keys up to its
+  // own; the planner takes the plan that it expects to be faster.
+  if (q8 && !items.empty() && cu[batch] <= kFewTokens &&
+      *std::max_element(extend_len, extend_len + batch) <= kFewPerRequest) {
+    const double expand_us = (double)tiles8.size() * hkv * kQ8ExpandBytes / 5e6;
+    const double tiles_us =
+        kQ8ExtendUs + expand_us + ends_at / 13.6 + (npart > 0 ? kMergeCost / 13.6 : 0.);
+    rx_plan few;
+    few.kv_next = RX_KV_E4M3;
+    if (few_tokens_plan(&few, desc, batch, req_idx, prefix_len, extend_len, grp, num_groups,
+                        group_prefix_len, group_parent) == RX_OK &&
+        few.hdr().n_xitems == 0 && few.q8_us < tiles_us) {
+      plan->blob.swap(few.blob);
+      plan->ws_bytes = few.ws_bytes;
+      plan->key_reads = few.key_reads;
+      plan->kind = 1;
+      remember_desc(plan, desc);
+      return RX_OK;
+    }
   }
 
   PlanHeader h;
@@ -1486,7 +1588,8 @@ rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const r
                       workspace_bytes);
   if (st) return st;
   const PlanHeader h = plan->hdr();
-  const int e = launch_extend_q8(desc, &h, kv, q, o, lse, workspace, stream);
+  const int e = h.kind == 2 ? launch_decode_q8(desc, &h, kv, q, o, lse, workspace, stream)
+                            : launch_extend_q8(desc, &h, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "extend launch") : RX_OK;
 }
 

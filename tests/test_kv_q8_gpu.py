@@ -669,6 +669,45 @@ def test_extend_cuts_items_where_the_lists_end_apart(cuda, hq, hkv, prefix, new,
     check_extend(pool, q, o[:rows], lse[:rows], prefix, new)
 
 
+@pytest.mark.parametrize("hq,hkv,prefix,new,groups", [
+    (32, 8, [3000, 700, 0, 129, 64], [1, 1, 1, 1, 1], []),
+    (48, 12, [2500] * 6, [2, 1, 3, 0, 17, 32], [((0, 1, 2, 3), 2400)]),
+    (5, 5, [1900, 2000, 2100], [4, 3, 2], [((0, 2), 1900)]),
+    (8, 1, [6000], [1], []),
+    (40, 5, [1500] * 5 + [1501], [1, 2, 1, 1, 2, 1], [((0, 1, 2, 3, 4, 5), 1500)])])
+def test_extend_of_few_new_tokens(cuda, hq, hkv, prefix, new, groups):
+    rng, pool, grp, gpl = extend_case(cuda, hq + sum(new), hq, hkv, prefix, new, groups)
+    q, o, lse, ws = run_extend(pool, rng, prefix, new, grp, gpl)
+    check_extend(pool, q, o, lse, prefix, new)
+    assert rx.read_status(ws) == rx.RX_OK
+    # planned as a decode: no expanded keys in the workspace
+    assert ws.numel() < sum(prefix[i] for i in range(len(new))) * hkv * 522 or sum(prefix) < 2000
+    pool.vs[pool.table[0, 1], 0] = np.nan  # a key that request 0 reads, and who shares it
+    pool.upload()
+    q2, o2, lse2, ws = run_extend(pool, rng, prefix, new, grp, gpl, q=q)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    for r in range(len(new)):
+        shares = r == 0 or (groups and r in groups[0][0])
+        got = o2[int(cu[r]):int(cu[r + 1])].float()
+        assert torch.isnan(got[:, :hq // hkv]).all() if shares and new[r] else not torch.isnan(got).any()
+    assert torch.isfinite(lse2).all()
+
+
+@pytest.mark.parametrize("hq,hkv,prefix,groups", [(32, 16, 2000, 3), (64, 8, 1500, 2)])
+def test_extend_splits_pairs_of_tiles(cuda, hq, hkv, prefix, groups):
+    """Fewer pairs of tiles than SMs, too many tiles to split each: the pairs' keys are split."""
+    members = 5
+    new = [20, 21, 3, 30, 26] * groups
+    if hq == 64:
+        new = [33, 40, 2, 61, 9] * groups
+    rng, pool, grp, gpl = extend_case(
+        cuda, hq, hq, hkv, [prefix + 7] * len(new), new,
+        [(range(g * members, (g + 1) * members), prefix) for g in range(groups)])
+    q, o, lse, ws = run_extend(pool, rng, [prefix + 7] * len(new), new, grp, gpl)
+    check_extend(pool, q, o, lse, [prefix + 7] * len(new), new)
+    assert rx.read_status(ws) == rx.RX_OK
+
+
 def test_extend_every_code_and_scale(cuda):
     """Codes of every value (subnormal ones too) and scales over 2^60."""
     prefix, new = [254], [64]

@@ -205,11 +205,33 @@ def test_extend_plan_for_the_8_bit_pool_reads_each_distinct_key_once(librx):
     assert plan.key_reads() == (gp + own) * hkv
     tiles = sum(-(-n // 64) for n in (gp, 100, 65, 700, 240))
     blocks = tiles * hkv * (2 * 64 * 256 + 2 * 64 * 4 + 128)
-    # (and, the batch being small, at most one partial tile of 128 rows per SM)
-    assert blocks <= plan.workspace_size() <= blocks + 160 * 128 * 516 + 65536
+    # (and, the batch being small, at most one partial pair of tiles of 128 rows per SM)
+    assert blocks <= plan.workspace_size() <= blocks + 160 * 256 * 516 + 65536
     bf = rx.Plan()
     rx.extend_plan(bf, desc, [0, 1, 2, 3, 4], prefix, new, [0, 0, 0, 0, -1], [gp])
     assert bf.workspace_size() < 65536 and bf.launches() == 1
+
+
+def test_extend_plan_of_few_new_tokens_needs_no_expansion(librx):
+    """One or two new tokens a request on long prefixes: planned as a decode of them, whose workspace
+    holds partial rows only.  The row count is the new tokens' all the same, and the plan serves
+    extend calls only."""
+    plan = rx.Plan()
+    plan.set_kv_type(rx.RX_KV_E4M3)
+    desc = _desc(32, 8, pool=1 << 20, rows=64, stride=8192)
+    new = [1, 2, 0, 1]
+    rx.extend_plan(plan, desc, [0, 1, 2, 3], [5000] * 4, new, [0, 0, 0, -1], [4000])
+    assert plan.rows() == 4 and plan.launches() == 2
+    # the group's prefix; the first's and the last's keys past it; the second's cached keys, and its
+    # new tokens' own
+    assert plan.key_reads() == (4000 + 1001 + 5001 + 1000 + 1 + 2) * 8
+    assert plan.workspace_size() < 1 << 23
+    with pytest.raises(rx.RxError) as e:
+        rx.decode_attn_q8(plan, desc, rx.KVQ8(4096, 4096, 4096, 4096), 4096, 4096, 4096, 4096,
+                          stream=0)
+    assert e.value.status == rx.RX_ERR_INVALID and "built for extend" in str(e.value)
+    rx.extend_plan(plan, desc, [0, 1, 2, 3], [5000] * 4, [200] * 4, [0, 0, 0, -1], [4000])
+    assert plan.workspace_size() > (4000 + 3 * 1000 + 5000) * 8 * 512
 
 
 def test_extend_plan_splits_the_keys_of_a_batch_too_small_for_the_gpu(librx):
