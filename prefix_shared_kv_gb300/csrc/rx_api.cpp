@@ -706,6 +706,46 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   std::vector<ExtSeg> xsegs;
   std::vector<Q8Tile> tiles8;  // 8-bit pool: the tiles of their keys, in the segments' order
   int64_t key_reads = 0;
+  // The tile items' longest list when list-scheduled, costliest first, with chunks of `keys` keys, in
+  // the units of attn_cost.
+  auto tiles_end = [&](int keys) {
+    std::vector<int64_t> costs;
+    for (int g = 0; g < num_groups; ++g) {
+      const int64_t tiles = ((int64_t)members[g].size() + tc_tok - 1) / tc_tok;
+      const int len = group_prefix_len[g] - node_lo(g);
+      if ((int64_t)members[g].size() * gq < kQ8TileRows || len <= 0) continue;
+      const int n = (len + keys - 1) / keys;
+      const int64_t steps = attn_steps((len + n - 1) / n);
+      for (int64_t i = 0; i < tiles; i += 2)
+        costs.insert(costs.end(), (size_t)n * hkv,
+                     steps * (i + 1 < tiles ? 14 : 11) + kItemCost + kCutCost);
+    }
+    std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> ends;
+    for (int k = 0; k < sms; ++k) ends.push(0);
+    int64_t longest = 0;
+    for (int64_t c : costs) {
+      const int64_t e = ends.top() + c;
+      ends.pop();
+      ends.push(e);
+      longest = std::max(longest, e);
+    }
+    return longest;
+  };
+  // 8-bit pool: the chunks' length by the earliest end (seven groups of 152 rows on 2,309 keys, 40/5
+  // heads, 35 items of 2,048: 89 us, 69 in shorter chunks; over 40 random batches with such groups 20 %
+  // less on the average, none slower)
+  int tile_keys = 2048;
+  if (q8) {
+    int64_t best = tiles_end(tile_keys);
+    for (int keys : {1536, 1024, 768, 512, 384, 256}) {
+      const int64_t end = tiles_end(keys);
+      if (end < best) {
+        best = end;
+        tile_keys = keys;
+      }
+    }
+  }
   for (int g = 0; g < num_groups; ++g) {
     const int lo = node_lo(g), hi = group_prefix_len[g];
     const auto& mem = members[g];
@@ -722,7 +762,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
         for (int i = 0; i < n_tok; ++i)
           xrows.push_back({mem[t0 + i], INT32_MAX, mem[t0 + i], 0});
       }
-      const int n_ch = std::max(1, (hi - lo + 1024) / 2048);
+      const int n_ch = q8 ? (hi - lo + tile_keys - 1) / tile_keys
+                          : std::max(1, (hi - lo + 1024) / 2048);
       const int clen = ((hi - lo + n_ch - 1) / n_ch + 63) / 64 * 64;
       for (int c0 = lo; c0 < hi; c0 += clen) {
         const int c1 = std::min(hi, c0 + clen);
