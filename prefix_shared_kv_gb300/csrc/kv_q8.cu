@@ -7,8 +7,9 @@
 // of zeros too.  Reading back is code * scale, rounded once to bf16.  A row with an infinity or a
 // NaN has no such scale: its scale is NaN and its codes 0, so it reads as NaN.
 //
-// Both kernels move data: 256 + 132 bytes a row.  Eight (store) or sixteen (load) lanes share a
-// row, so that a lane's wider side is 16-byte accesses and a row's maximum takes three shuffles;
+// Both kernels move data: 256 + 132 bytes a row.  Eight lanes share a row, so that a lane's bf16 side
+// is a 32-byte access (two of 16 where the tensor is not 32-byte aligned), its codes a 16-byte one,
+// and a row's maximum takes three shuffles;
 // K and V are the two halves of the grid's y axis, and a thread has the loads of all its rows in
 // flight before the first is used.
 #include <cuda_bf16.h>
