@@ -708,6 +708,65 @@ def test_extend_splits_pairs_of_tiles(cuda, hq, hkv, prefix, groups):
     assert rx.read_status(ws) == rx.RX_OK
 
 
+def test_every_form_of_extend_captured_and_on_two_streams(cuda):
+    """Few new tokens, cut items and split pairs: three plans captured in one graph, replayed with new
+    queries, and called on two streams at once, give what eager calls give, bit for bit."""
+    rng = np.random.default_rng(31)
+    forms = [(8, 2, [3000, 500], [1, 2]), (24, 3, [1500], [830]), (16, 16, [1200] * 2, [150, 149])]
+    made = []
+    for hq, hkv, prefix, new in forms:
+        lens = [p + e for p, e in zip(prefix, new)]
+        n = sum(lens) + 20
+        pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens))
+        plan = rx.Plan()
+        plan.set_kv_type(rx.RX_KV_E4M3)
+        rx.extend_plan(plan, pool.desc, np.arange(len(new)), prefix, new)
+        ws = workspace(plan.workspace_size(), cuda)
+        plan.upload(ws)
+        rows = sum(new)
+        made.append((pool, plan, ws, torch.empty(rows, hq, 128, dtype=torch.bfloat16, device=cuda),
+                     torch.empty(rows, hq, 128, dtype=torch.bfloat16, device=cuda),
+                     torch.empty(rows, hq, device=cuda)))
+
+    def call(m):
+        pool, plan, ws, q, o, lse = m
+        rx.extend_attn_q8(plan, pool.desc, pool.kv, q, o, lse, ws)
+
+    def fresh(seed):
+        g = torch.Generator(device=cuda).manual_seed(seed)
+        for m in made:
+            m[3].copy_(torch.randn(m[3].shape, generator=g, device=cuda))
+            m[4].fill_(7)
+            m[5].fill_(7)
+
+    def results():
+        torch.cuda.synchronize()
+        return [t.clone() for m in made for t in m[4:]]
+
+    want = []
+    for seed in (1, 2):
+        fresh(seed)
+        for m in made:
+            call(m)
+        want.append(results())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for m in made:
+            call(m)
+    for seed in (1, 2, 1):
+        fresh(seed)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want[seed - 1]))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    fresh(2)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, m in enumerate(made):
+            with torch.cuda.stream(streams[i % 2]):
+                call(m)
+    assert all(torch.equal(a, b) for a, b in zip(results(), want[1]))
+
+
 def test_extend_every_code_and_scale(cuda):
     """Codes of every value (subnormal ones too) and scales over 2^60."""
     prefix, new = [254], [64]
