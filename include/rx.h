@@ -154,8 +154,8 @@ rx_status rx_plan_set_kv_type(rx_plan* plan, int32_t kv_type);
 /* Number of kernels one attention call with the built plan launches (0 for a plan without work;
  * a decode plan launches up to three: tensor-core shared-prefix units, mma.sync units, merge; over
  * an 8-bit pool an extend launches two, expansion and attention, and a merge if tiles' keys are
- * split, one of few new tokens what a decode does; a decode up to five: expansion and attention of very large groups, wide items, narrow items,
- * merge).
+ * split, one of few new tokens what a decode does; a decode up to five: expansion and attention of
+ * very large groups, wide items, narrow items, merge).
  * For a caller's and a benchmark's bookkeeping; (host). */
 rx_status rx_plan_launches(const rx_plan* plan, int32_t* launches);
 /* Rows of q / o / lse an attention call with the built plan reads and writes: the sum of
