@@ -479,8 +479,10 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
             }
             // a column moves when it has to itself: another request's scores are no reason
             if (!(x1 > m_old + 8.f || x2 > m2_old + 8.f)) continue;
-            // c = 2^en with weights of at most about 1; none while every V scale was 0
-            const int en = x2 == kUnset ? -127 : (int)rintf(fminf(fmaxf(x1 - x2, -126.f), 126.f));
+            // c = 2^en with weights of at most about 1.  The largest c while every V scale was 0 or
+            // subnormal (lg2 flushes those): O is still 0, or as small as such scales make it, and
+            // the first scale of any size either gives weights that fp16 holds or moves c.
+            const int en = x2 == kUnset ? 126 : (int)rintf(fminf(fmaxf(x1 - x2, -126.f), 126.f));
             ls[j] *= fast_exp2(m_old - x1);
             const float a = w[j] == 0.f ? 0.f : fast_exp2(m_old - x1 + (float)(en - ew));
 #pragma unroll

@@ -1,0 +1,123 @@
+"""Attention over an 8-bit pool whose scales the library's own store does not write: zeros, subnormal
+numbers and runs of entries outside the pool.  Bounds as in test_kv_q8_gpu; a key of V scale 0 has no
+part in them but in the sum of the softmax."""
+import numpy as np
+import pytest
+import torch
+
+from prefix_shared_kv_gb300 import rx
+from test_kv_q8_gpu import (Pool, check_decode, check_extend, extend_case, random_table, run_decode,
+                            run_extend)
+
+pytestmark = pytest.mark.gpu
+
+ZEROED = ["zero", "subnormal", "outside"]
+
+
+def level(pool):
+    """Scores within a few powers of two of one another: no later key stands out."""
+    pool.ks *= np.float32(0.25)
+
+
+def drop_v(pool, table_rows, first, last, how):
+    """Keys first .. last - 1 of the requests in `table_rows` (which share them) without a V."""
+    at = pool.table[table_rows[0], first:last]
+    if how == "outside":
+        for r in table_rows:
+            pool.table[r, first:last] = -1
+    else:
+        pool.vs[at] = 0.0 if how == "zero" else np.float32(2.0 ** -130)
+
+
+def crowded(cuda, rng, hq, hkv, lens, gone, how, shared=None):
+    """A pool of 2,400 slots over which many requests' tables run, so that items are several steps
+    long: each request (or, in `shared`, each group's prefix) begins with gone[b] slots without V."""
+    without, n = 400, 2400
+    pool = Pool(cuda, rng, hq, hkv, n, np.zeros((len(lens), max(lens)), np.int32))
+    level(pool)
+    pool.vs[:without] = 0.0 if how == "zero" else np.float32(2.0 ** -130)
+
+    def row(length, first):
+        first = min(first, length)
+        head = np.full(first, -1) if how == "outside" else rng.permutation(without)[:first]
+        return np.concatenate([head, without + rng.permutation(n - without)[:length - first]])
+
+    for b, length in enumerate(lens):
+        pool.table[b, :length] = row(length, 0 if shared else gone[b])
+    for members, prefix, first in shared or ():
+        pool.table[list(members), :prefix] = row(prefix, first)
+    pool.upload()
+    return pool
+
+
+@pytest.mark.parametrize("how", ZEROED)
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 2), (8, 2), (8, 8), (32, 8), (6, 3), (8, 1)])
+def test_decode_of_requests_that_begin_without_v(cuda, hq, hkv, how):
+    """The first 32 (one warp's first step), 64, 256, 300 or all keys of a request have no V."""
+    rng = np.random.default_rng(100 + hq + hkv)
+    gone = ([32, 64, 300, 400, 0, 256] * 60)[:1200 // hkv + 100]
+    lens = [400 if g == 400 else int(x)
+            for g, x in zip(gone, rng.integers(1200, 2000, len(gone)))]
+    pool = crowded(cuda, rng, hq, hkv, lens, gone, how)
+    q, o, lse, ws, _ = run_decode(pool, rng, lens)
+    assert rx.read_status(ws) == (rx.RX_ERR_RANGE if how == "outside" else rx.RX_OK)
+    check_decode(pool, q, o, lse, lens, range(8))
+    if how != "subnormal":
+        assert (o[3] == 0).all()
+
+
+@pytest.mark.parametrize("how", ["zero", "outside"])
+@pytest.mark.parametrize("hq,hkv,members", [(8, 8, 12), (16, 2, 6), (8, 1, 5), (4, 4, 40),
+                                            (32, 8, 16)])
+def test_decode_of_shared_prefixes_that_begin_without_v(cuda, hq, hkv, members, how):
+    """Groups of 10 to 64 rows a KV head: the narrow and the wide form, whole and split stages."""
+    rng = np.random.default_rng(200 + hq + hkv + members)
+    groups = 100 if hkv < 4 else 30
+    first = [32, 300, 64, 0, 256] * (groups // 5)
+    shared = [(range(g * members, (g + 1) * members), 1500, first[g]) for g in range(groups)]
+    lens = [1500 + int(x) for x in rng.integers(0, 20, groups * members)]
+    pool = crowded(cuda, rng, hq, hkv, lens, None, how, shared)
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, np.repeat(np.arange(groups), members),
+                                  [1500] * groups)
+    assert rx.read_status(ws) == (rx.RX_ERR_RANGE if how == "outside" else rx.RX_OK)
+    check_decode(pool, q, o, lse, lens, [0, members - 1, members, 2 * members + 1, 4 * members])
+
+
+@pytest.mark.parametrize("how", ZEROED)
+def test_decode_without_v_in_the_middle_and_in_turns(cuda, how):
+    rng = np.random.default_rng(300)
+    lens = [900, 900]
+    pool = Pool(cuda, rng, 8, 2, 2000, random_table(rng, 2000, lens))
+    level(pool)
+    drop_v(pool, [0], 200, 700, how)
+    for k in range(0, 900, 64):
+        drop_v(pool, [1], k, k + 32, how)
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens)
+    check_decode(pool, q, o, lse, lens)
+
+
+@pytest.mark.parametrize("how", ZEROED)
+@pytest.mark.parametrize("hq,hkv,new", [(32, 8, [1, 1]), (48, 12, [2, 3]), (8, 1, [1, 2])])
+def test_extend_of_few_new_tokens_that_begins_without_v(cuda, hq, hkv, new, how):
+    """Plans that run as a decode."""
+    prefix = [3000, 2500]
+    rng, pool, _, _ = extend_case(cuda, 400 + hq, hq, hkv, prefix, new)
+    level(pool)
+    drop_v(pool, [0], 0, 32, how)
+    drop_v(pool, [1], 0, 300, how)
+    pool.upload()
+    q, o, lse, ws = run_extend(pool, rng, prefix, new)
+    assert ws.numel() < sum(prefix) * hkv * 522  # no expanded keys
+    check_extend(pool, q, o, lse, prefix, new)
+
+
+@pytest.mark.parametrize("how", ZEROED)
+def test_extend_on_tiles_that_begins_without_v(cuda, how):
+    prefix, new = [500, 40], [200, 90]
+    rng, pool, _, _ = extend_case(cuda, 500, 8, 2, prefix, new)
+    drop_v(pool, [0], 0, 300, how)
+    drop_v(pool, [1], 0, 32, how)
+    pool.upload()
+    q, o, lse, ws = run_extend(pool, rng, prefix, new)
+    check_extend(pool, q, o, lse, prefix, new)
