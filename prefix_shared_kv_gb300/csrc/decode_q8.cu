@@ -9,8 +9,8 @@
 // tell on another request's scores, have no part in it (unless all are that large, and within
 // 2^16): a warp computes them in fp32 by themselves when it is done with the others.
 // With p_j = 2^(s_j - m), m a running reference of the row, the sum takes p_j and the
-// second product's weights are p_j vs_j c, c a power of two of the row that keeps them at 2^8 or
-// less whatever the scales are: fp16 holds them to 2^-11 of their value down to 2^-14, and to
+// second product's weights are p_j vs_j c, c a power of two of the row that keeps their magnitude at
+// 2^8 or less whatever the scales (of either sign) are: fp16 holds them to 2^-11 of their value down to 2^-14, and to
 // 2^-25 below.  m and c only move (and O is only rescaled) when some p_j or weight of the warp's
 // passes 2^8, which one vote per step decides; until then a step needs no maximum across lanes.
 //
@@ -427,7 +427,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
       }
       uint32_t pt[KT][NT][2];  // P^T: columns are query rows, two keys a register
       uint64_t add[NT];
-      auto weigh = [&]() {  // weights and sums under the present references; the largest
+      auto weigh = [&]() {  // weights and sums under the present references; the largest magnitude
         float top = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -445,7 +445,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
               add[n] = f2_add(add[n], e);
               f2_unpack(f2_mul(f2_mul(e, f2_pack(vs[t][h], vs[t][h])), cw[n]), w0, w1);
               top = fmax3(top, e0, e1);
-              top = fmax3(top, w0, w1);
+              top = fmax3(top, fabsf(w0), fabsf(w1));
               pt[t][n][h] = pack_f16(w0, w1);
             }
         }
@@ -470,7 +470,7 @@ __device__ __forceinline__ bool run_item(const Params& p, const DecItem& it, uin
               for (int h = 0; h < 2; ++h) {
                 const float v = s[t][n][2 * h + j] * kq[t][h];
                 x1 = fmaxf(x1, v);
-                x2 = fmaxf(x2, v + lg2(vs[t][h]));
+                x2 = fmaxf(x2, v + lg2(fabsf(vs[t][h])));
               }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
