@@ -98,7 +98,7 @@ constexpr int kQTile = 2 * kQHalf;     // 32 KiB
 constexpr int kKVHalf = kN * 128;      // one 64-column half of a 64-key K or V tile: 8 KiB
 constexpr int kKVTile = 2 * kKVHalf;   // 16 KiB
 constexpr int kScRing = 8;             // steps in the ring of scales (8-bit pool)
-constexpr int kScStep = 2 * kN * 4 + 16;  // K scales, V scales and the NaN word of a step's keys
+constexpr int kScStep = 2 * kN * 4 + 16;  // K and V scales of a step's keys, and their word (Q8Tile)
 // TMEM columns: S buffers S_A0, S_A1, S_B0, S_B1 of 64 columns from 0 (P_x(t), 64 bf16 a row, two
 // a column, over the upper half of S_x's buffer t % 2), O_A [256,384), O_B [384,512)
 constexpr uint32_t kTmemCols = 512;
@@ -669,12 +669,13 @@ static __device__ __forceinline__ bool softmax_steps(const ExtParams& p, const E
     uint64_t acc[2] = {0ull, 0ull};
     row_exp(sr, pk, acc, scales + 4 * kN);
     if constexpr (Q8) {
-      // a masked key's P is 0 whatever its V scale is (0 * NaN is not; the word says whether the
-      // step has such a scale: without it this loop cost 7 % on batches with many masked steps)
-      uint32_t nan = 0;
+      // a masked key's P is 0 whatever its V scale is (0 times an infinity or a NaN is not; the word
+      // says whether the step has such a scale: without it this loop cost 7 % on batches with many
+      // masked steps)
+      uint32_t special = 0;
       if (n_ok < kN)
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(nan) : "r"(scales + 8 * kN) : "memory");
-      if (nan) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(special) : "r"(scales + 8 * kN) : "memory");
+      if (special) {
 #pragma unroll
         for (int e = 0; e < kN; e += 2)
           pk[e >> 1] = e + 1 < n_ok ? pk[e >> 1] : e < n_ok ? pk[e >> 1] & 0xffffu : 0u;

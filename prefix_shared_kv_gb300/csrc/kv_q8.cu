@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     float scale_log2, const Q8Tile* __restrict__ tiles, uint8_t* __restrict__ stage,
     int32_t* status) {
   __shared__ int32_t s_slot[kAttnKeys];
-  __shared__ uint32_t s_nan[kExpandHeads];
+  __shared__ uint32_t s_special[kExpandHeads];
   const Q8Tile tile = tiles[blockIdx.x];
   const int head0 = blockIdx.y * kExpandHeads, nh = min(kExpandHeads, hkv - head0);
   wait_for_predecessors();
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     }
     s_slot[threadIdx.x] = s;
   }
-  if (threadIdx.x < kExpandHeads) s_nan[threadIdx.x] = 0;
+  if (threadIdx.x < kExpandHeads) s_special[threadIdx.x] = 0;
   __syncthreads();
   let_successors_start();
   uint8_t* blocks = stage + ((int64_t)blockIdx.x * hkv + head0) * kQ8BlockBytes;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
     sc[0] = ok ? __ldg(k_scale + row) * scale_log2 : 0.f;
     const float v = ok ? __ldg(v_scale + row) : 0.f;
     sc[kQ8BlockV / 4] = v;
-    if (isnan(v)) s_nan[h] = 1;  // (every writer writes the same)
+    if (!isfinite(v)) s_special[h] = 1;  // (every writer writes the same)
   }
   const int n = kAttnKeys * nh * 8;
   constexpr int U = 4;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) expand_q8_kernel(
   __syncthreads();
   if ((int)threadIdx.x < nh)
     *reinterpret_cast<uint32_t*>(blocks + (int64_t)threadIdx.x * kQ8BlockBytes + 2 * kQ8BlockV) =
-        s_nan[threadIdx.x];
+        s_special[threadIdx.x];
 }
 
 int sm_count() {

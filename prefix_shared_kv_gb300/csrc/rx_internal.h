@@ -93,7 +93,8 @@ constexpr int kPairKeys = 128;
 // tile (its step i reads tile kv_row + i).  Block (tile, KV head), at tile * Hkv + head: the K
 // operand's shared-memory image (bf16 codes, two 64-column halves of 128-byte-swizzled rows), the
 // keys' K scales times softmax_scale * log2(e), the V operand's image, the keys' V scales, and a
-// word that is not 0 if one of the V scales is NaN.  Keys past the segment are zeros with scale 0.
+// word that is not 0 if one of the V scales is an infinity or a NaN.  Keys past the segment are
+// zeros with scale 0.
 struct Q8Tile {
   int32_t kv_row;        // req_to_token row
   int32_t k_begin;

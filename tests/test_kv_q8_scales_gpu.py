@@ -167,3 +167,38 @@ def test_extend_of_negative_scales(cuda):
         pool.upload()
         q, o, lse, ws = run_extend(pool, rng, prefix, new)
         check_extend(pool, q, o, lse, prefix, new)
+
+
+FORMS = [  # an extend on whole tiles (shared and own keys), with split keys, with cut items
+    (8, 4, [100, 100, 30], [70, 20, 40], [(range(2), 100)]),
+    (8, 2, [1000] * 4, [40] * 4, [(range(4), 1000)]),
+    (24, 3, [2500], [830], [])]
+
+
+@pytest.mark.parametrize("scale", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("hq,hkv,prefix,new,groups", FORMS)
+def test_extend_scales_of_keys_a_row_does_not_see_do_not_reach_it(cuda, hq, hkv, prefix, new, groups,
+                                                                  scale):
+    """The last new token of request 0 and a middle one of the last request have scales that are not
+    finite: the rows before them, and the other requests' rows, are as before, bit for bit."""
+    rng, pool, grp, gpl = extend_case(cuda, 800 + hq + sum(new), hq, hkv, prefix, new, groups)
+    q, o, lse, ws = run_extend(pool, rng, prefix, new, grp, gpl)
+    check_extend(pool, q, o, lse, prefix, new)
+    last = len(new) - 1
+    mid = new[last] // 2
+    pool.vs[pool.table[0, prefix[0] + new[0] - 1]] = scale
+    pool.vs[pool.table[last, prefix[last] + mid]] = scale
+    pool.upload()
+    _, o2, lse2, _ = run_extend(pool, rng, prefix, new, grp, gpl, q=q)
+    sees = torch.zeros(len(o), dtype=torch.bool)
+    sees[new[0] - 1] = True
+    sees[len(o) - new[last] + mid:] = True
+    assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2, lse)
+    assert not torch.isfinite(o2[sees].float()).any()  # (code 0 of such a key: 0 * inf, NaN)
+    pool.vs[pool.table[0, prefix[0] + new[0] - 1]] = 1
+    pool.vs[pool.table[last, prefix[last] + mid]] = 1
+    pool.ks[pool.table[0, prefix[0] + new[0] - 1]] = scale
+    pool.ks[pool.table[last, prefix[last] + mid]] = scale
+    pool.upload()
+    _, o2, lse2, _ = run_extend(pool, rng, prefix, new, grp, gpl, q=q)
+    assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2[~sees], lse[~sees])
