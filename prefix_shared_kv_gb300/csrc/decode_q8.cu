@@ -79,7 +79,6 @@ constexpr int kThreads = 32 * kWarps + kProducers;
 // Registers: the launch's 168 a thread; the wide form moves them to its consumers.
 constexpr int kRegsLaunch = 168, kRegsConsumer = 232, kRegsProducer = 40;
 static_assert(2 * kRegsConsumer + kRegsProducer == 3 * kRegsLaunch, "register split");
-constexpr int kNoKey = INT32_MIN;  // past an item's keys
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kUnset = -1e30f;   // a reference no score has moved yet
 
@@ -139,7 +138,7 @@ __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const int key = k0 + 32 * i + lane;
-        nxt[i] = key < nkeys ? __ldg(table + key) : kNoKey;
+        nxt[i] = key < nkeys ? __ldg(table + key) : -1;
       }
     };
     fetch(0);
@@ -150,8 +149,8 @@ __device__ void producer(const Params& p, uint32_t base, volatile int* abort) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         sl[i] = nxt[i];
-        if (sl[i] < 0 || sl[i] >= p.pool_size) {  // flagged, and read as zeros
-          if (sl[i] != kNoKey) atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
+        if (sl[i] < 0 || sl[i] >= p.pool_size) {  // a key's: flagged, and read as zeros
+          if (k0 + 32 * i + lane < nkeys) atomicCAS(p.status, 0, (int)RX_ERR_RANGE);
           sl[i] = -1;
         }
       }

@@ -202,3 +202,19 @@ def test_extend_scales_of_keys_a_row_does_not_see_do_not_reach_it(cuda, hq, hkv,
     pool.upload()
     _, o2, lse2, _ = run_extend(pool, rng, prefix, new, grp, gpl, q=q)
     assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2[~sees], lse[~sees])
+
+
+@pytest.mark.parametrize("bad", [-2 ** 31, -2 ** 31 + 1, -1, 2 ** 31 - 1])
+@pytest.mark.parametrize("hq,hkv,members", [(8, 2, 1), (32, 8, 16), (8, 1, 20)])
+def test_decode_flags_every_entry_outside_the_pool(cuda, hq, hkv, members, bad):
+    """The narrow, the wide and the tile form; no entry stands for "no key"."""
+    rng = np.random.default_rng(900 + members)
+    lens = [200 + b for b in range(members)]
+    n = 200 + sum(lens) + 10
+    pool = Pool(cuda, rng, hq, hkv, n, random_table(rng, n, lens, {0: (list(range(members)), 200)}))
+    pool.table[:, 133] = bad
+    pool.upload()
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, [0] * members, [200])
+    assert rx.read_status(ws) == rx.RX_ERR_RANGE and rx.read_status(ws) == rx.RX_OK
+    check_decode(pool, q, o, lse, lens, [0, members - 1],
+                 EXT_ERR if members * hq // hkv > 128 else DEC_ERR)
