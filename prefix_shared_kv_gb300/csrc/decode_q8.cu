@@ -80,7 +80,7 @@ constexpr int kThreads = 32 * kWarps + kProducers;
 constexpr int kRegsLaunch = 168, kRegsConsumer = 232, kRegsProducer = 40;
 static_assert(2 * kRegsConsumer + kRegsProducer == 3 * kRegsLaunch, "register split");
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kUnset = -1e30f;   // a reference no score has moved yet
+constexpr float kUnset = -3.402823466e38f;  // a reference no score has moved yet: the lowest float
 
 // HB = 1 << HBL KV heads a block.
 template <bool WIDE, int HBL>

@@ -5,7 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import attention as A, quantised as Q
 from prefix_shared_kv_gb300 import rx
+from prefix_shared_kv_gb300.session import bits_of
 from test_kv_q8_gpu import (DEC_ERR, EXT_ERR, Pool, check_decode, check_extend, extend_case,
                             random_table, run_decode, run_extend)
 
@@ -218,3 +220,41 @@ def test_decode_flags_every_entry_outside_the_pool(cuda, hq, hkv, members, bad):
     assert rx.read_status(ws) == rx.RX_ERR_RANGE and rx.read_status(ws) == rx.RX_OK
     check_decode(pool, q, o, lse, lens, [0, members - 1],
                  EXT_ERR if members * hq // hkv > 128 else DEC_ERR)
+
+
+@pytest.mark.parametrize("size", [90, 101, 120])
+@pytest.mark.parametrize("hq,hkv,members", [(8, 2, 1), (32, 8, 16), (8, 1, 20)])
+def test_decode_of_scores_far_below_zero(cuda, hq, hkv, members, size):
+    """Scores of -2^size and keys at twice that, which weigh nothing, in either order: large K rows that
+    point away from the query."""
+    rng = np.random.default_rng(1000 + members)
+    n_keys = 400
+    lens = [n_keys] * members + [n_keys, 40]
+    n = sum(lens) + 10
+    pool = Pool(cuda, rng, hq, hkv, n,
+                random_table(rng, n, lens, {0: (list(range(members)), n_keys)}))
+    pool.scale = 0.125
+    pool.kc[:], pool.ks[:] = 0, np.float32(2.0 ** (size + 3))
+    pool.kc[:, :, 0] = 0xB8                                   # -1
+    pool.kc[pool.table[0, 200:n_keys], :, 0] = 0xC0           # -2: of no weight
+    pool.kc[pool.table[members, :200], :, 0] = 0xC0
+    pool.upload()
+    q = np.zeros((len(lens), hq, 128), np.uint16)
+    q[:, :, 0] = 0x3F80                                       # 1
+    q, o, lse, ws, _ = run_decode(pool, rng, lens, [0] * members + [-1, -1], [n_keys], q=q)
+    assert rx.read_status(ws) == rx.RX_OK
+    for b, seen in ((0, range(200)), (members - 1, range(200)), (members, range(200, n_keys)),
+                    (members + 1, range(40))):
+        at = pool.table[b, list(seen)]
+        v = np.repeat(Q.values(pool.vc[at], pool.vs[at]), hq // hkv, axis=1)
+        # A partial result's log-sum-exp is -2^size / ln 2 + log2(its keys) in float32, whose steps
+        # there are 2^(size - 23): the count is lost, and partials of unlike counts are merged as
+        # equals.  What is left of the definition is that o is a mean of the keys' rows with weights
+        # of sum 1: it lies between their extremes, but for the roundings of weights and output.
+        err = EXT_ERR if members * hq // hkv > 128 else DEC_ERR
+        tol = (2.0 ** -8 + err + 2.0 ** -18) * 1.01 * np.abs(v).max(0)
+        got = A.bf16_to_f64(bits_of(o[b]))
+        assert ((got >= v.min(0) - tol) & (got <= v.max(0) + tol)).all() and (got != 0).any(), b
+        # -2^size + log of the count, which float32 cannot tell from -2^size
+        got = lse[b].double().cpu().numpy()
+        assert (np.abs(got + 2.0 ** size) <= 2.0 ** (size - 22)).all(), b
