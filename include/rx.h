@@ -190,9 +190,9 @@ rx_status rx_plan_upload(const rx_plan* plan, void* workspace, size_t workspace_
  * prefix_len[r]); the kernel then reads that prefix KV once for all new rows of the group.  -1 (or
  * group_of_req == NULL) declares no sharing.  The result does not depend on the grouping.
  * All arrays of rx_extend_plan are (host).  extend_len[r] == 0 is allowed; sum of extend_len must
- * be < 2^31.  batch == 0 builds a plan with no work: the attention call then enqueues nothing and
- * may be given NULL tensors.  o needs 16-byte alignment; at 32-byte alignment rows are written in
- * 32-byte pieces.
+ * be < 2^31.  A batch without new tokens (batch == 0, or every extend_len 0) builds a plan with no
+ * work: the attention call then enqueues nothing and may be given NULL tensors.  o needs 16-byte
+ * alignment; at 32-byte alignment rows are written in 32-byte pieces.
  * On the default kernel (rx_plan_set_extend_kernel) the plan deals its work items into one list
  * per SM of the calling thread's current GPU (152 where no GPU is visible); the attention call
  * launches one CTA per list, so the plan runs on any GPU, at its best on one with as many SMs.

@@ -243,6 +243,9 @@ rx_status check_kv_q8(const rx_kv_q8* kv) {
   return RX_OK;
 }
 
+// Whether a built plan's attention call has rows; without any it enqueues nothing and takes no tensors.
+bool has_rows(const PlanHeader& h) { return h.n_items > 0 || (h.kind == 2 && h.batch > 0); }
+
 rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_kv_desc* d,
                          const void* k,
                          const void* v, const void* q, const void* o, const void* lse,
@@ -258,8 +261,7 @@ rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_k
   if (d->num_q_heads != p->hq || d->num_kv_heads != p->hkv || d->req_to_token_rows != p->rows ||
       d->req_to_token_stride != p->stride || d->pool_size != p->pool)
     return fail(RX_ERR_INVALID, "descriptor differs from the one the plan was built with");
-  const PlanHeader h = p->hdr();
-  if (h.n_items > 0 || (h.kind == 2 && h.batch > 0)) {  // an extend plan without new tokens has no rows
+  if (has_rows(p->hdr())) {
     if (!k || !v || !q || !o || !lse) return fail(RX_ERR_INVALID, "NULL tensor pointer");
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(o) || !aligned16(lse))
       return fail(RX_ERR_INVALID, "tensors must be 16-byte aligned");
@@ -270,6 +272,17 @@ rx_status check_plan_use(const rx_plan* p, int kind, int32_t kv_type, const rx_k
   if (ws_bytes < p->ws_bytes)
     return fail(RX_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, p->ws_bytes);
   return RX_OK;
+}
+
+// check_plan_use for a call over an 8-bit pool.
+rx_status check_plan_use_q8(const rx_plan* p, int kind, const rx_kv_desc* d, const rx_kv_q8* kv,
+                            const void* q, const void* o, const void* lse, const void* ws,
+                            size_t ws_bytes) {
+  const bool no_rows = p && p->kind == kind && !has_rows(p->hdr());
+  const rx_status st = no_rows ? RX_OK : check_kv_q8(kv);
+  if (st) return st;
+  return check_plan_use(p, kind, RX_KV_E4M3, d, kv ? kv->k_code : nullptr,
+                        kv ? kv->v_code : nullptr, q, o, lse, ws, ws_bytes);
 }
 
 }  // namespace
@@ -967,12 +980,11 @@ rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
 rx_status rx_decode_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream) {
-  rx_status st = check_kv_q8(kv);
-  if (st) return st;
-  st = check_plan_use(plan, 2, RX_KV_E4M3, desc, kv->k_code, kv->v_code, q, o, lse, workspace,
-                      workspace_bytes);
+  const rx_status st =
+      check_plan_use_q8(plan, 2, desc, kv, q, o, lse, workspace, workspace_bytes);
   if (st) return st;
   const PlanHeader h = plan->hdr();
+  if (!has_rows(h)) return RX_OK;
   const int e = launch_decode_q8(desc, &h, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "decode launch") : RX_OK;
 }
@@ -1623,12 +1635,11 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
 rx_status rx_extend_attn_q8(const rx_plan* plan, const rx_kv_desc* desc, const rx_kv_q8* kv,
                             const void* q, void* o, float* lse, void* workspace,
                             size_t workspace_bytes, rx_stream_t stream) {
-  rx_status st = check_kv_q8(kv);
-  if (st) return st;
-  st = check_plan_use(plan, 1, RX_KV_E4M3, desc, kv->k_code, kv->v_code, q, o, lse, workspace,
-                      workspace_bytes);
+  const rx_status st =
+      check_plan_use_q8(plan, 1, desc, kv, q, o, lse, workspace, workspace_bytes);
   if (st) return st;
   const PlanHeader h = plan->hdr();
+  if (!has_rows(h)) return RX_OK;
   const int e = h.kind == 2 ? launch_decode_q8(desc, &h, kv, q, o, lse, workspace, stream)
                             : launch_extend_q8(desc, &h, kv, q, o, lse, workspace, stream);
   return e ? cuda_fail(e, "extend launch") : RX_OK;

@@ -246,3 +246,37 @@ def test_extend_plan_splits_the_keys_of_a_batch_too_small_for_the_gpu(librx):
     desc = _desc(32, 32, pool=1 << 20, rows=64, stride=4096)
     rx.extend_plan(plan, desc, np.arange(32), [1000] * 32, [200] * 32)
     assert plan.launches() == 2
+
+
+@pytest.mark.parametrize("new", [[], [0], [0, 0]])
+def test_calls_without_rows_take_no_tensors(librx, new):
+    """A plan without work enqueues nothing: its call may be given NULL tensors and pools, and still
+    needs the right plan, descriptor and workspace."""
+    desc = _desc()
+    null, part = rx.KVQ8(0, 0, 0, 0), rx.KVQ8(4096, 0, 4096, 8)
+    for kv_type in (rx.RX_KV_BF16, rx.RX_KV_E4M3):
+        plan = rx.Plan()
+        plan.set_kv_type(kv_type)
+        if new:
+            rx.extend_plan(plan, desc, np.arange(len(new)), [5] * len(new), new)
+            bf16, q8 = librx.rx_extend_attn, librx.rx_extend_attn_q8
+        else:
+            rx.decode_plan(plan, desc, np.zeros(0, np.int32), np.zeros(0, np.int32))
+            bf16, q8 = librx.rx_decode_attn, librx.rx_decode_attn_q8
+        for ws, size, status in ((0x1000, 1 << 20, rx.RX_OK), (0x1000, 8, rx.RX_ERR_WORKSPACE),
+                                 (None, 1 << 20, rx.RX_ERR_WORKSPACE),
+                                 (0x1010, 1 << 20, rx.RX_ERR_INVALID)):
+            if kv_type == rx.RX_KV_BF16:
+                # (RX_ERR_CUDA: past the checks, the kernels' attributes need a GPU)
+                got = bf16(plan.handle, C.byref(desc), None, None, None, None, None, ws, size, None)
+                assert got == status or (status == rx.RX_OK and got == rx.RX_ERR_CUDA)
+                assert q8(plan.handle, C.byref(desc), None, None, None, None, ws, size,
+                          None) == rx.RX_ERR_INVALID
+            else:
+                for kv in (None, C.byref(null), C.byref(part)):
+                    assert q8(plan.handle, C.byref(desc), kv, None, None, None, ws, size,
+                              None) == status
+    plan = _decode_plan(rx.RX_KV_E4M3, desc, [5])  # with rows every pointer is looked at
+    for kv in (None, C.byref(null), C.byref(part)):
+        assert librx.rx_decode_attn_q8(plan.handle, C.byref(desc), kv, 4096, 4096, 4096, 0x1000,
+                                       1 << 30, None) == rx.RX_ERR_INVALID
