@@ -598,13 +598,16 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   auto kind_of_rows = [&](int r) {
     return q8 ? (r > kQ8MaxRows ? 2 : r > 8) : r <= 16 ? 0 : (r <= 32 ? 1 : 2);
   };
-  auto hb_of = [&](int kind) {
-    return q8 ? (kind == 2 ? q8_whb : q8_hb) : kind == 0 ? 8 : (kind == 1 ? 4 : 2);
-  };
-  auto splits_of = [&](int kind) { return !q8 ? 1 : (kind == 2 ? 4 : 8) / hb_of(kind); };
-  auto stage_keys = [&](int kind) {  // keys of a pipeline stage
-    return q8 ? splits_of(kind) * kQ8WarpKeys : kDecRows / hb_of(kind);
-  };
+  // by kind: heads a block, partial results a unit, keys of a pipeline stage (looked up per item and
+  // per comparison of the sorts below)
+  const int hbs[3] = {q8 ? q8_hb : 8, q8 ? q8_hb : 4, q8 ? q8_whb : 2};
+  const int splits[3] = {q8 ? 8 / hbs[0] : 1, q8 ? 8 / hbs[1] : 1, q8 ? 4 / hbs[2] : 1};
+  const int stages_keys[3] = {q8 ? splits[0] * kQ8WarpKeys : kDecRows / hbs[0],
+                              q8 ? splits[1] * kQ8WarpKeys : kDecRows / hbs[1],
+                              q8 ? splits[2] * kQ8WarpKeys : kDecRows / hbs[2]};
+  auto hb_of = [&](int kind) { return hbs[kind]; };
+  auto splits_of = [&](int kind) { return splits[kind]; };
+  auto stage_keys = [&](int kind) { return stages_keys[kind]; };
 
   // The units' keys: a shared prefix for a tile of its members, then each request's own.
   struct Span {
@@ -705,7 +708,8 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   std::vector<std::pair<int, int>> ch;
   // The references of one request to a unit of `len` keys: one partial per split that has keys.
   auto refer = [&](int b, int kind, int64_t part, int len, int n_rows, int row) {
-    for (int k = 0; k < splits_of(kind) && k * kQ8WarpKeys < len; ++k)
+    refs[b].push_back({(int32_t)part, n_rows, row, 0});
+    for (int k = 1; k < splits_of(kind) && k * kQ8WarpKeys < len; ++k)
       refs[b].push_back({(int32_t)(part + (int64_t)k * hkv * n_rows), n_rows, row, 0});
   };
 
@@ -854,15 +858,23 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
                       (int32_t)u.part});
     key_reads += (int64_t)(u.k_end - u.k_begin) * hkv;
   }
-  auto cost = [&](const DecItem& it) {
-    return q8 ? (double)item_cost(it.kind, it.n_tok * gq,
-                                  (it.k_end - it.k_begin + stage_keys(it.kind) - 1) /
-                                      stage_keys(it.kind))
-              : (double)(it.k_end - it.k_begin) * std::min(hb_of(it.kind), hkv);
+  auto cost = [&](const DecItem& it) {  // 8-bit pool
+    return (double)item_cost(it.kind, it.n_tok * gq,
+                             (it.k_end - it.k_begin + stage_keys(it.kind) - 1) /
+                                 stage_keys(it.kind));
   };
   auto by_cost = [&](const DecItem& a, const DecItem& b) { return cost(a) > cost(b); };
-  std::stable_sort(items.begin(), items.end(), by_cost);
-  std::stable_sort(wide.begin(), wide.end(), by_cost);
+  // bf16 pool: by keys times heads
+  auto by_rows = [&](const DecItem& a, const DecItem& b) {
+    return (int64_t)(a.k_end - a.k_begin) * std::min(hbs[a.kind], hkv) >
+           (int64_t)(b.k_end - b.k_begin) * std::min(hbs[b.kind], hkv);
+  };
+  if (q8) {
+    std::stable_sort(items.begin(), items.end(), by_cost);
+    std::stable_sort(wide.begin(), wide.end(), by_cost);
+  } else {
+    std::stable_sort(items.begin(), items.end(), by_rows);
+  }
 
   // 8-bit pool: one list per CTA, each item (costliest first) to the list that is shortest so
   // far; the table is stored list by list
