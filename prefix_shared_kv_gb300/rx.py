@@ -158,11 +158,25 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+_torch_calls = None
+
+
+def _cuda_calls():
+    """The current device, and the raw handle of a device's current stream: torch's private calls, where
+    it has them (building its Stream object costs as much as the rest of a call), or the public ones."""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch
+        _torch_calls = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                        getattr(torch._C, "_cuda_getCurrentRawStream",
+                                lambda device: torch.cuda.current_stream(device).cuda_stream))
+    return _torch_calls
+
+
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        # the raw handle: building torch's Stream object costs as much as the rest of a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _cuda_calls()[1](torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -239,7 +253,7 @@ def _call_q8(fn, desc: KVDesc, kv: KVQ8, named, args, stream):
                              f"{(desc.pool_size, desc.num_kv_heads, desc.head_dim)}")
         if kv.device < 0:
             raise ValueError("the pool's tensors are not CUDA tensors")
-        device = torch._C._cuda_getDevice()
+        device = _cuda_calls()[0]()
         if kv.device != device:
             raise ValueError(f"the pool is on device {kv.device}, the current device is {device}")
     else:
@@ -252,8 +266,7 @@ def _call_q8(fn, desc: KVDesc, kv: KVQ8, named, args, stream):
             raise ValueError(f"{name}: {n} contiguous elements of {dtype} on CUDA device {device} "
                              f"expected, got {t.numel()} of {t.dtype} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
-    st = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None
-            else _stream(stream))
+    st = fn(*args, _cuda_calls()[1](device) if stream is None else _stream(stream))
     if st != RX_OK:
         _check(st)
 

@@ -280,3 +280,14 @@ def test_calls_without_rows_take_no_tensors(librx, new):
     for kv in (None, C.byref(null), C.byref(part)):
         assert librx.rx_decode_attn_q8(plan.handle, C.byref(desc), kv, 4096, 4096, 4096, 0x1000,
                                        1 << 30, None) == rx.RX_ERR_INVALID
+
+
+def test_the_current_stream_is_found_without_torchs_private_call(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(rx, "_torch_calls", None, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    assert rx._stream(None) == 77 and rx._stream(5) == 5 and rx._stream(Stream) == 77
