@@ -838,7 +838,7 @@ int launch_merge_q8(const rx_kv_desc* d, const PlanHeader* h, int32_t n, void* o
   // One warp a row up to 8 partials, two up to 32, else eight; sixteen for no more rows than SMs (52
   // rows of some 130 partials: the call takes 12.6 us, with eight warps 14.5; 300 rows: 40.0 us, with
   // eight 38.0)
-  const bool few = (int64_t)n * hq <= 152;
+  const bool few = (int64_t)n * hq <= h->n_sms;
   return (int)(h->max_refs <= 8    ? launch_merge<1>(base, h, n, hq, gq, o, lse, s)
                : h->max_refs <= 32 ? launch_merge<2>(base, h, n, hq, gq, o, lse, s)
                : few               ? launch_merge<16>(base, h, n, hq, gq, o, lse, s)

@@ -2,15 +2,16 @@
 //
 // A row is the 128 values of one (token, KV head) of K or of V.  With a = max |x| over the row:
 //   scale = max(a / 448, 2^-126),  code = e4m3(x * r),  r = 448 / a  (2^126 at the scale's floor),
-// so the largest value takes the largest code, 448, and every code is within half an e4m3 step of
-// x / scale.  448 is e4m3's largest value; the floor keeps scale and r normal numbers, for a row
-// of zeros too.  Reading back is code * scale, rounded once to bf16.  A row with an infinity or a
-// NaN has no such scale: its scale is NaN and its codes 0, so it reads as NaN.
+// so the largest value takes the largest code, 448.  A code is within half an e4m3 step of x / scale
+// but for the float32 roundings of scale, r and x r (together 3 x 2^-24 of the value): a value that
+// close to a tie may go to either side of it.  448 is e4m3's largest value; the floor keeps scale and
+// r normal numbers, for a row of zeros too.  Reading back is code * scale, rounded once to bf16.  A
+// row with an infinity or a NaN has no such scale: its scale is NaN and its codes 0, so it reads as
+// NaN.
 //
 // Both kernels move data: 256 + 132 bytes a row.  Eight lanes share a row, so that a lane's bf16 side
 // is a 32-byte access (two of 16 where the tensor is not 32-byte aligned), its codes a 16-byte one,
-// and a row's maximum takes three shuffles;
-// K and V are the two halves of the grid's y axis, and a thread has the loads of all its rows in
+// and a row's maximum takes three shuffles; K and V are the two halves of the grid's y axis, and a thread has the loads of all its rows in
 // flight before the first is used.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -317,8 +318,9 @@ int sm_count() {
 // Launch shapes (GB300, K and V each).  Many rows: four a thread in flight and two CTAs per SM;
 // 13,064 tokens x 32 heads stored take 53.5 us so, 54.9 with two rows a thread, 58.4 with four CTAs
 // per SM; 32,003 x 32 read back 124.7 us, 129.6 with four CTAs, 126.6 with two rows and four CTAs.
-// Few rows, up to what the GPU holds at once with one row a thread: one, and as many CTAs as that
-// makes; 40 tokens x 32 heads stored take 1.9 us so, 3.4 with four rows a thread.
+// Few rows, up to what the GPU holds at once with one row per eight lanes (32 a CTA, four of an SM's
+// eight CTAs for K and four for V): one, and as many CTAs as that makes; 40 tokens x 32 heads stored
+// take 1.6 us so, 3.0 with four rows.
 constexpr int kManyRows = 4, kManyCtas = 2;
 bool few_rows(int64_t rows, int sms) { return rows <= (int64_t)sms * (2048 / kThreads / 2) * (kThreads / 8); }
 

@@ -947,6 +947,7 @@ static rx_status decode_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   h.n_wide = (int32_t)wide.size();
   h.n_wide_ctas = wide_begin.empty() ? 0 : (int32_t)wide_begin.size() - 1;
   h.max_refs = max_refs;
+  h.n_sms = sms;
   const size_t tables = off;
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
   h.off_part_lse = off; off = align256(off + (size_t)npart * 4);
@@ -1609,6 +1610,7 @@ static rx_status extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t
   h.off_merge_rows = off; off = align256(off + merge_rows.size() * sizeof(MergeRow));
   h.n_merge_rows = (int64_t)merge_rows.size();
   h.max_refs = max_refs;
+  h.n_sms = device_sms();
   plan->blob.assign(off, 0);
   h.off_part_o = off; off = align256(off + (size_t)npart * kHeadDim * 4);
   h.off_part_lse = off; off = align256(off + (size_t)npart * 4);

@@ -159,7 +159,9 @@ struct PlanHeader {
   // MergeRow (n_merge_rows = 0: it writes every row, each by its entry of the merge index)
   int64_t off_merge_rows;
   int64_t n_merge_rows;
-  int64_t pad[5];
+  int32_t n_sms;         // plans for the 8-bit pool: the GPU's SMs when it was built
+  int32_t pad32;
+  int64_t pad[4];
 };
 static_assert(sizeof(PlanHeader) == 256, "header is 256 bytes");
 
