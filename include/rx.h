@@ -96,8 +96,9 @@ rx_status rx_store_kv(const rx_kv_desc* desc, void* k_pool, void* v_pool, const 
  * slots, same req_to_token table, calls of its own.  All (device), caller-owned, 16-byte aligned:
  *   k_code, v_code    [pool_size, num_kv_heads, head_dim] e4m3
  *   k_scale, v_scale  [pool_size, num_kv_heads] float32
- * Value x of a row stands for code * scale.  What the calls below read holds no NaN codes (0x7f,
- * 0xff); a NaN scale makes its whole row NaN. */
+ * Value x of a row stands for code * scale, whatever float32 number the scale is (the store writes
+ * positive ones; zeros and negative ones of another quantiser read as they stand).  What the calls
+ * below read holds no NaN codes (0x7f, 0xff); a NaN scale makes its whole row NaN. */
 typedef struct {
   void* k_code;
   void* v_code;
@@ -109,8 +110,8 @@ typedef struct {
  * rx_store_kv (k_new, v_new bf16).  Per row of 128 values, with a = max |x|:
  *   scale = max(a / 448, 2^-126),   code = e4m3(x * r), round to nearest even, saturating,
  * where r = 448 / a in float32 (2^126 at the scale's floor).  A row with an infinity or a NaN gets
- * scale NaN and codes 0.  Out-of-pool and duplicate slots as rx_store_kv (a duplicate's row is one
- * writer's codes, and one writer's scale: they need not be the same writer's). */
+ * scale NaN and codes 0.  Out-of-pool slots as rx_store_kv; the codes and scale of a slot that is named
+ * twice are unspecified (they may mix its writers'). */
 rx_status rx_store_kv_q8(const rx_kv_desc* desc, const rx_kv_q8* kv, const void* k_new,
                          const void* v_new, const int32_t* slots, int64_t num_tokens,
                          rx_stream_t stream);
@@ -209,13 +210,15 @@ rx_status rx_extend_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
  * (the new tokens' KV stored there with rx_store_kv_q8 first):
  *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
- * with fp32 sums of exact products of the codes.  Scales of keys a row does not see, NaN ones
- * included, do not reach it.  pool_size * num_kv_heads is not limited.
- * A plan of few new tokens (at most 32 a request) that would be faster as a decode of them runs as
- * rx_decode_attn_q8 does, each new token a request with the keys up to its own.  Otherwise
- * the call first expands each distinct key of the plan into its workspace, once for all the query
- * tiles that read it: rx_plan_workspace_size is about 522 bytes per distinct key and KV head (each
- * shared prefix and each request's own keys rounded up to 64).  A batch whose tiles would leave SMs
+ * with fp32 sums; query and codes enter their products exactly, the scales in fp32.  Rounded are the
+ * second product's weights softmax_j v_scale_j, to bf16 (2^-8 of their value), and o.  Scales of keys
+ * a row does not see, infinities and NaN included, do not reach it.  pool_size * num_kv_heads is not
+ * limited.
+ * A plan of few new tokens (at most 32 a request) that is expected to be faster as a decode of them
+ * runs as rx_decode_attn_q8 does, with its roundings, each new token a request with the keys up to its
+ * own.  Otherwise the call first expands each distinct key of the plan into its workspace, once for
+ * all the query tiles that read it: rx_plan_workspace_size is about 522 bytes per distinct key and KV
+ * head (each shared prefix and each request's own keys rounded up to 64).  A batch whose tiles would leave SMs
  * idle (a few new tokens on a long prefix) has the tiles' keys split over the SMs and merged, one
  * whose SMs would end far apart those of some tiles; each part of a row and query head so split takes
  * 516 bytes of workspace. */
@@ -285,7 +288,13 @@ rx_status rx_decode_attn(const rx_plan* plan, const rx_kv_desc* desc, const void
 /* rx_decode_attn_q8 -- rx_decode_attn over an 8-bit pool, for a decode plan built for RX_KV_E4M3:
  *   s_j = softmax_scale * k_scale_j * (q . k_code_j),
  *   o = sum_j softmax_j v_scale_j v_code_j,   lse = log sum_j exp(s_j),
- * with fp32 sums of exact products of the codes.  A key whose K scale is NaN makes o and lse of
+ * with fp32 sums; the codes enter their products exactly, the scales in fp32.  Rounded are the query,
+ * to fp16 by a power of two common to the query rows that are computed together (an element is off by
+ * less than 2^-39 of the largest magnitude among them; rows with magnitudes of 2^20 and more are
+ * computed apart in fp32), the second product's weights softmax_j v_scale_j, to fp16 (2^-11 of their
+ * value; those below 2^-14 of a row's largest, 2^-25 of that), and o.  The shared prefix of more
+ * than 128 stacked query rows runs on the extend's kernel, with its roundings (weights to bf16, 2^-8;
+ * the query exact): a request's roundings depend on how many share its prefix.  A key whose K scale is NaN makes o and lse of
  * the requests that read it NaN, a NaN V scale their o.  The shared prefix of up to 64 stacked query
  * rows (requests x query heads per KV head) is read once, of up to 128 once per 64; that of a
  * larger group is read once and expanded into the workspace (522 bytes per key and KV head). */

@@ -1035,8 +1035,10 @@ rx_status rx_extend_plan_tree(rx_plan* plan, const rx_kv_desc* desc, int32_t bat
 }
 
 // 8-bit pool: extends of at most this many new tokens, in all and of a request, are also planned as a
-// decode (16 requests of one or two new tokens in pairs on 5,715, 48/12 heads: 36.8 us, expanded and
-// on tiles 172; 10 of up to 17 on 715, 12/12 heads: 17.0 and 14.8, on tiles).
+// decode, and the plan with the lower estimate is taken.  The estimates miss by up to a quarter and no
+// margin is asked for, so where both are close the slower may win (16 requests of one or two new tokens
+// in pairs on 5,715, 48/12 heads: 36.8 us, expanded and on tiles 172; 10 of up to 17 on 715, 12/12
+// heads: 17.0 and 14.8, on tiles).
 constexpr int64_t kFewTokens = 2048;
 constexpr int32_t kFewPerRequest = 32;
 // A step's keys in the expansion (read, and written), and what an extend's launches take beyond a

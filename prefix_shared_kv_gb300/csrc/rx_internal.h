@@ -56,8 +56,9 @@ constexpr size_t kDecSmemBytes = (size_t)kDecStages * kDecStageBytes + kDecMaxKe
 constexpr int kQ8WarpKeys = 32;
 // A shared prefix of kQ8TileRows stacked rows or more goes to the tensor-core tile kernel instead,
 // 256 rows at a time, its keys expanded first.  (8 groups on 8,000 tokens, 8 tokens at most of their
-// own, 8 KV heads, whole call, wide items against tiles: 96 rows 148 / 169 us, 128 rows 160 / 171, 160
-// rows 238 / 198, 192 rows 245 / 213; 4 groups of 256 rows 159 / 113, 2 of 512 158 / 94.)
+// own, 8 KV heads, whole call, wide items against tiles: 96 rows 149 / 170 us, 128 rows 161 / 172, 130
+// rows 180 / 201, 160 rows 239 / 199, 192 rows 246 / 214, 256 rows 266 / 218, 300 rows 373 / 314; 4
+// groups of 256 rows 159 / 114, 2 of 512 159 / 95.)
 constexpr int kQ8MaxRows = 16, kQ8MaxWideRows = 64, kQ8TileRows = 129;
 inline int q8_head_block_log2(int hkv) {
   return hkv % 8 == 0 ? 3 : hkv % 4 == 0 ? 2 : hkv % 2 == 0 ? 1 : 0;
